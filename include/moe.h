@@ -492,6 +492,110 @@ moe_status moe_forward_expert_choice(const void* x, const void* Wg, const float*
                                      void* y, void* ws, size_t ws_bytes, moe_stats* stats,
                                      void* stream);
 
+/* ------------------------------------------------------------- training
+ * What stands around the experts' own products in a training step: the
+ * load-balancing loss, the combine with dropout and the residual, and the
+ * backward passes of the combine and of the router.  A step in order:
+ *
+ *     moe_route, moe_expert_choice_route (scores), moe_balance_loss,
+ *     moe_permute, moe_grouped_ffn, moe_combine_dropout
+ *     -- y and the loss; then, from dy and the loss's gradient --
+ *     moe_combine_dropout_backward  -> d_o (for the experts), dgate
+ *     moe_route_backward            -> dx, dWg, dbias
+ *
+ * With the experts frozen that is every gradient the router needs.  The
+ * experts' own gradient dxp of the permuted tokens returns to the tokens by
+ * moe_unpermute_combine with gates of one; its result is the dx_acc of
+ * moe_route_backward.
+ *
+ * mask [T] (uint8, nullable): 0 marks a padding token.  It is counted
+ * nowhere and gets no gradient; its x row and scores are not looked at, so
+ * they may hold anything (NaN too).
+ * Every sum is in fp32 and in an order that does not depend on scheduling
+ * (no floating-point atomics): the same call gives the same bits.  Buffers
+ * must not overlap unless said below; nothing is kept between calls, so
+ * calls may run at once on different streams with workspaces of their own. */
+
+/* The router's load-balancing loss ("How do Mixture of Expert Models Work?",
+ * "Load Balancing": an auxiliary loss so that the experts get about the same
+ * number of training examples; here the Switch Transformer's product of each
+ * expert's share of the assignments and its mean probability):
+ *     L = coef * E * sum_e (counts_e / (N k)) * (prob_sum_e / N)
+ * over the N counted tokens; coef when the experts are used evenly.
+ *   scores [E, T] as from moe_expert_choice_route, idx [T, k] as from
+ *   moe_route (an index outside 0 .. E - 1 is counted nowhere), T k < 2^31.
+ *   Out (device): loss [1] fp32; prob_sum [E] fp32 = sum over the counted
+ *   tokens of scores; counts [E] int32 = their assignments (before any
+ *   capacity); tokens [1] int32 = N.  With N == 0 (T == 0 too) all are 0.
+ *   ws: at least moe_balance_loss_workspace_bytes(T, E).
+ * Its gradient is part of moe_route_backward.  For a batch split over ranks,
+ * add up counts, tokens and prob_sum over the ranks: the loss is the formula
+ * on the sums, and moe_route_backward takes the summed counts and tokens. */
+size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E);
+moe_status moe_balance_loss(const float* scores, const int32_t* idx, const uint8_t* mask,
+                            int32_t T, int32_t E, int32_t k, float coef, float* loss,
+                            float* prob_sum, int32_t* counts, int32_t* tokens, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Backward pass of the router (moe_route_ex) and of moe_balance_loss.  With
+ * g the gates, s the gate scale, p the scores and f_e = counts_e / (N k),
+ * the gradient dz of the logits of a counted token is the sum of
+ *   gates, MOE_GATE_TOPK_SOFTMAX: at idx_j   g_j (dg_j - sum_i (g_i / s) dg_i)
+ *   gates, MOE_GATE_SOFTMAX_TOPK: at idx_j   g_j dg_j, and everywhere
+ *                                 - p_e sum_i g_i dg_i
+ *   loss:  dloss coef (E / N) p_e (f_e - sum_i f_i p_i)
+ *   x [T, d], Wg [d, E] (dtype); scores [E, T] (may be NULL where neither
+ *   counts nor MOE_GATE_SOFTMAX_TOPK reads it); idx, gate, dgate [T, k] or
+ *   dgate NULL: nothing through the gates (idx and gate are then not read;
+ *   an idx outside 0 .. E - 1 adds nothing at its place);
+ *   counts [E] and tokens [1] (N) as from moe_balance_loss, or both NULL:
+ *   nothing from the loss.  dloss: device fp32 [1], or NULL for 1; coef, opt
+ *   (gating, gate_scale) as in the forward pass.
+ *   Out, each NULL if not wanted: dx [T, d] (dtype) = dx_acc + dz Wg^T,
+ *   rounded once (dx_acc [T, d] (dtype) or NULL for 0; dx may be dx_acc; a
+ *   padding token's row is its dx_acc); dWg [d, E] fp32 = x^T dz; dbias [E]
+ *   fp32 = sum over the tokens of dz.  x may be NULL without dWg, Wg without
+ *   dx.  T == 0 gives dWg = dbias = 0.
+ *   ws: at least moe_route_backward_workspace_bytes(T, d, E, dtype). */
+size_t moe_route_backward_workspace_bytes(int32_t T, int32_t d, int32_t E, moe_dtype dtype);
+moe_status moe_route_backward(const void* x, const void* Wg, const float* scores,
+                              const int32_t* idx, const float* gate, const float* dgate,
+                              const int32_t* counts, const int32_t* tokens, const float* dloss,
+                              float coef, const uint8_t* mask, const void* dx_acc, int32_t T,
+                              int32_t d, int32_t E, int32_t k, moe_dtype dtype,
+                              const moe_options* opt, void* dx, float* dWg, float* dbias,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* moe_unpermute_combine with dropout of the layer's output and the residual:
+ *     y_tc = residual_tc + m_tc * sum_j gate[t,j] o[pos[t,j], c]
+ * accumulated in fp32 and rounded once.  residual [T, d] (dtype) or NULL for
+ * 0; y may be the residual.  m is 0 for a dropped element (which is left out,
+ * whatever o holds there) and 1 / (1 - p) for the others.
+ * p: 0 <= p < 1, taken to the nearest multiple of 2^-16 (at most 1 - 2^-16).
+ * rng: device uint64 [2] = {seed, offset}, read when the kernel runs, so a
+ * captured graph drops other elements once the caller changes it; may be
+ * NULL when p rounds to 0.  Element c of token t takes 16 bits of
+ * Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2,
+ * 3", 2011) with key seed and counter {(t d + c) / 8 (64 bits), offset (64
+ * bits)}: of the four words, word (c % 8) / 2, its low half for even c; it
+ * is dropped below p * 2^16.  The mask is stored nowhere: the backward pass
+ * makes it again from the same rng and p. */
+moe_status moe_combine_dropout(const void* o, const int32_t* pos, const float* gate,
+                               const void* residual, double p, const uint64_t* rng, int32_t T,
+                               int32_t d, int32_t k, moe_dtype dtype, void* y, void* stream);
+
+/* Backward pass of moe_combine_dropout (p = 0: of moe_unpermute_combine),
+ * with a_tc = m_tc dy_tc:
+ *   d_o [rows, d] (dtype): row pos[t,j] = gate[t,j] * a_t, rounded once;
+ *     rows that no kept slot owns are left as they were.
+ *   dgate [T, k] fp32 = sum over the elements c that were not dropped of
+ *     a_tc o[pos[t,j], c], 0 for a slot that was dropped (pos -1).
+ * The residual's gradient is dy itself. */
+moe_status moe_combine_dropout_backward(const void* dy, const void* o, const int32_t* pos,
+                                        const float* gate, double p, const uint64_t* rng,
+                                        int32_t T, int32_t d, int32_t k, moe_dtype dtype,
+                                        void* d_o, float* dgate, void* stream);
+
 /* ------------------------------------------------------ measurement aid
  * No counterpart on the pages: a yardstick for the HBM-bound stages.  Reads
  * `bytes` of the device buffer `buf` once with streaming 16-byte loads (two

@@ -1036,6 +1036,142 @@ MOE_API moe_status moe_forward_expert_choice(const void* x, const void* Wg, cons
   return stats->device_error ? MOE_ERR_DEVICE : MOE_OK;
 }
 
+// =============================================================== training
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The drop probability in units of 2^-16, and the kept elements' scale.
+bool read_dropout(double p, const uint64_t* rng, uint32_t* threshold, float* scale) {
+  if (!(p >= 0.0 && p < 1.0)) return false;
+  *threshold = std::min(static_cast<uint32_t>(p * 65536.0 + 0.5), 65535u);
+  *scale = static_cast<float>(65536.0 / (65536.0 - *threshold));
+  return *threshold == 0 || (rng && (reinterpret_cast<uintptr_t>(rng) & 7u) == 0);
+}
+
+bool valid_combine_sizes(int32_t T, int32_t d, int32_t k, moe_dtype dt) {
+  return T >= 0 && d > 0 && d % 8 == 0 && k >= 1 && k <= kMaxK && valid_dtype(dt);
+}
+
+}  // namespace
+
+MOE_API size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E) {
+  return T < 0 || E < 1 || E > kMaxE ? 0 : balance_scratch_bytes(T);
+}
+
+MOE_API moe_status moe_balance_loss(const float* scores, const int32_t* idx, const uint8_t* mask,
+                                    int32_t T, int32_t E, int32_t k, float coef, float* loss,
+                                    float* prob_sum, int32_t* counts, int32_t* tokens, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  if (T < 0 || E < 1 || E > kMaxE || k < 1 || k > kMaxK || k > E || !isfinite(coef) ||
+      static_cast<int64_t>(T) * k > INT32_MAX)
+    return MOE_ERR_ARG;
+  if (!loss || !prob_sum || !counts || !tokens || !aligned4(loss) || !aligned4(prob_sum) ||
+      !aligned4(counts) || !aligned4(tokens))
+    return MOE_ERR_ARG;
+  if (!ws || !aligned16(ws) || ws_bytes < balance_scratch_bytes(T)) return MOE_ERR_ARG;
+  if (T > 0 && (!scores || !idx || !aligned4(scores) || !aligned4(idx))) return MOE_ERR_ARG;
+  DeviceInfo di;
+  moe_status st = device_info(&di);
+  if (st != MOE_OK) return st;
+  BalanceArgs a{scores, idx, mask, T, E, k, coef, loss, prob_sum, counts, tokens, ws};
+  return launch_balance_loss(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
+                                                                                  : MOE_ERR_CUDA;
+}
+
+MOE_API size_t moe_route_backward_workspace_bytes(int32_t T, int32_t d, int32_t E, moe_dtype dt) {
+  return valid_route_sizes(T, d, E, 1) && valid_dtype(dt)
+             ? route_backward_scratch_bytes(T, d, E, dt)
+             : 0;
+}
+
+MOE_API moe_status moe_route_backward(const void* x, const void* Wg, const float* scores,
+                                      const int32_t* idx, const float* gate, const float* dgate,
+                                      const int32_t* counts, const int32_t* tokens,
+                                      const float* dloss, float coef, const uint8_t* mask,
+                                      const void* dx_acc, int32_t T, int32_t d, int32_t E,
+                                      int32_t k, moe_dtype dt, const moe_options* opt, void* dx,
+                                      float* dWg, float* dbias, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  int gating;
+  float gate_scale;
+  if (!valid_route_sizes(T, d, E, k) || !valid_dtype(dt) ||
+      !read_options(opt, &gating, &gate_scale) || !isfinite(coef))
+    return MOE_ERR_ARG;
+  if (!aligned16(dx) || !aligned16(dWg) || !aligned4(dbias)) return MOE_ERR_ARG;
+  if (!counts != !tokens || !aligned4(counts) || !aligned4(tokens) || !aligned4(dloss))
+    return MOE_ERR_ARG;
+  if (T > 0) {  // an empty batch's [T, ...] buffers may be NULL
+    // A gradient through the gates, from the loss, or both, to somewhere.
+    if ((!dgate && !counts) || (!dx && !dWg && !dbias)) return MOE_ERR_ARG;
+    if (dgate && (!idx || !gate || !aligned4(idx) || !aligned4(gate) || !aligned4(dgate)))
+      return MOE_ERR_ARG;
+    if ((counts || gating == MOE_GATE_SOFTMAX_TOPK) && (!scores || !aligned4(scores)))
+      return MOE_ERR_ARG;
+    if (dx && (!Wg || !aligned16(Wg) || !aligned16(dx_acc))) return MOE_ERR_ARG;
+    if (dWg && (!x || !aligned16(x))) return MOE_ERR_ARG;
+    if (!ws || !aligned16(ws) || ws_bytes < route_backward_scratch_bytes(T, d, E, dt))
+      return MOE_ERR_ARG;
+  }
+  if (T == 0 && !dWg && !dbias) return MOE_OK;
+  DeviceInfo di;
+  moe_status st = device_info(&di);
+  if (st != MOE_OK) return st;
+  RouteBackwardArgs a{x,      Wg,   scores, idx,        gate, dgate, counts, tokens, dloss, mask,
+                      dx_acc, coef, gating, gate_scale, T,    d,     E,      k,      dx,    dWg,
+                      dbias,  ws};
+  return launch_route_backward(a, dt, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+MOE_API moe_status moe_combine_dropout(const void* o, const int32_t* pos, const float* gate,
+                                       const void* residual, double p, const uint64_t* rng,
+                                       int32_t T, int32_t d, int32_t k, moe_dtype dt, void* y,
+                                       void* stream) {
+  uint32_t threshold;
+  float scale;
+  if (!valid_combine_sizes(T, d, k, dt) || !read_dropout(p, rng, &threshold, &scale))
+    return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;
+  if (!o || !pos || !gate || !y || !aligned16(o) || !aligned16(residual) || !aligned16(y) ||
+      !aligned4(pos) || !aligned4(gate))
+    return MOE_ERR_ARG;
+  DeviceInfo di;
+  moe_status st = device_info(&di);
+  if (st != MOE_OK) return st;
+  CombineDropoutArgs a{o, pos, gate, rng, threshold, scale, T, d, k};
+  a.residual = residual;
+  a.y = y;
+  return launch_combine_dropout(a, dt, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+MOE_API moe_status moe_combine_dropout_backward(const void* dy, const void* o, const int32_t* pos,
+                                                const float* gate, double p, const uint64_t* rng,
+                                                int32_t T, int32_t d, int32_t k, moe_dtype dt,
+                                                void* d_o, float* dgate, void* stream) {
+  uint32_t threshold;
+  float scale;
+  if (!valid_combine_sizes(T, d, k, dt) || !read_dropout(p, rng, &threshold, &scale))
+    return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;
+  if (!dy || !o || !pos || !gate || !d_o || !dgate || !aligned16(dy) || !aligned16(o) ||
+      !aligned16(d_o) || !aligned4(pos) || !aligned4(gate) || !aligned4(dgate))
+    return MOE_ERR_ARG;
+  DeviceInfo di;
+  moe_status st = device_info(&di);
+  if (st != MOE_OK) return st;
+  CombineDropoutArgs a{o, pos, gate, rng, threshold, scale, T, d, k};
+  a.dy = dy;
+  a.d_o = d_o;
+  a.dgate = dgate;
+  return launch_combine_dropout_backward(a, dt, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
 MOE_API moe_status moe_probe_stream_read(const void* buf, size_t bytes, uint32_t* sink,
                                          void* stream) {
   if (bytes == 0) return MOE_OK;

@@ -579,6 +579,66 @@ struct CombineArgs {
 };
 cudaError_t launch_combine(const CombineArgs& a, moe_dtype dtype, cudaStream_t s);
 
+// Combine with dropout and residual, and its backward pass (combine_dropout.cu).
+struct CombineDropoutArgs {
+  const void* o;           // [rows, d] in the layer dtype
+  const int32_t* pos;
+  const float* gate;
+  const uint64_t* rng;     // {seed, offset} in device memory; unused when threshold == 0
+  uint32_t threshold;      // drop probability in units of 2^-16 (0: no dropout)
+  float scale;             // 1 / (1 - p) of the kept elements
+  int T, d, k;
+  const void* residual = nullptr;  // forward: [T, d] or null
+  void* y = nullptr;               // forward: may be the residual
+  const void* dy = nullptr;        // backward
+  void* d_o = nullptr;             // backward: kept rows written, the others untouched
+  float* dgate = nullptr;          // backward: [T, k]
+};
+cudaError_t launch_combine_dropout(const CombineDropoutArgs& a, moe_dtype dtype, cudaStream_t s);
+cudaError_t launch_combine_dropout_backward(const CombineDropoutArgs& a, moe_dtype dtype,
+                                            cudaStream_t s);
+
+// Load-balancing loss (balance.cu).
+struct BalanceArgs {
+  const float* scores;     // [E, T]
+  const int32_t* idx;      // [T, k]
+  const uint8_t* mask;     // [T] or null
+  int T, E, k;
+  float coef;
+  float* loss;
+  float* prob_sum;
+  int32_t* counts;
+  int32_t* tokens;
+  void* ws;
+};
+size_t balance_scratch_bytes(int T);
+cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s);
+
+// Router backward pass (route_backward.cu).
+struct RouteBackwardArgs {
+  const void* x;           // null when dWg is not wanted
+  const void* Wg;          // null when dx is not wanted
+  const float* scores;     // [E, T]; null where no term reads it
+  const int32_t* idx;
+  const float* gate;
+  const float* dgate;      // null: no gradient through the gates
+  const int32_t* counts;   // null: no gradient from the balance loss
+  const int32_t* tokens;
+  const float* dloss;      // null: 1
+  const uint8_t* mask;     // [T] or null
+  const void* dx_acc;      // [T, d] or null
+  float coef;
+  int gating;
+  float gate_scale;
+  int T, d, E, k;
+  void* dx;                // null: not wanted (so dWg and dbias)
+  float* dWg;
+  float* dbias;
+  void* ws;
+};
+size_t route_backward_scratch_bytes(int T, int d, int E, moe_dtype dtype);
+cudaError_t launch_route_backward(const RouteBackwardArgs& a, moe_dtype dtype, cudaStream_t s);
+
 // Measurement aid (probe.cu): read `bytes` (a multiple of 16) of `buf` once
 // with streaming 16-byte loads; one XOR word per warp lands in *sink.
 cudaError_t launch_stream_read(const void* buf, size_t bytes, uint32_t* sink, int num_sms,

@@ -1,0 +1,54 @@
+// The counter-based generator behind dropout: Philox4x32-10 (Salmon, Moraes,
+// Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011).  Ten
+// rounds of two 32x32 -> 64 bit products turn a 128-bit counter and a 64-bit
+// key into four independent 32-bit words, so any thread can make the numbers
+// of any element on its own and a mask never has to be stored.
+#pragma once
+
+#include <stdint.h>
+
+namespace moe {
+
+__host__ __device__ __forceinline__ void philox_round(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
+  const uint64_t a = static_cast<uint64_t>(0xD2511F53u) * c[0];
+  const uint64_t b = static_cast<uint64_t>(0xCD9E8D57u) * c[2];
+  c[0] = static_cast<uint32_t>(b >> 32) ^ c[1] ^ k0;
+  c[1] = static_cast<uint32_t>(b);
+  c[2] = static_cast<uint32_t>(a >> 32) ^ c[3] ^ k1;
+  c[3] = static_cast<uint32_t>(a);
+}
+
+// The four words of counter (n, offset) under key `seed`.
+__host__ __device__ __forceinline__ void philox4x32_10(uint64_t n, uint64_t offset, uint64_t seed,
+                                                       uint32_t (&c)[4]) {
+  c[0] = static_cast<uint32_t>(n);
+  c[1] = static_cast<uint32_t>(n >> 32);
+  c[2] = static_cast<uint32_t>(offset);
+  c[3] = static_cast<uint32_t>(offset >> 32);
+  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    philox_round(c, k0, k1);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
+// Dropout's decision for eight consecutive elements (element group n): bit i
+// is set where element 8 n + i is kept.  16 random bits an element, so one
+// call covers a 16-byte vector of bf16 and the drop probability is a multiple
+// of 2^-16: dropped below `threshold` (0 .. 65535).
+__host__ __device__ __forceinline__ uint32_t dropout_keep8(uint64_t n, uint64_t offset,
+                                                           uint64_t seed, uint32_t threshold) {
+  uint32_t w[4];
+  philox4x32_10(n, offset, seed, w);
+  uint32_t keep = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    keep |= ((w[i] & 0xffffu) >= threshold ? 1u : 0u) << (2 * i);
+    keep |= ((w[i] >> 16) >= threshold ? 1u : 0u) << (2 * i + 1);
+  }
+  return keep;
+}
+
+}  // namespace moe

@@ -37,6 +37,9 @@ EXPORTED = (
     "moe_pipeline_submit", "moe_pipeline_wait", "moe_pipeline_destroy",
     "moe_forward_graph_create", "moe_forward_graph_launch", "moe_forward_graph_destroy",
     "moe_forward_graph_nodes",
+    "moe_balance_loss_workspace_bytes", "moe_balance_loss",
+    "moe_route_backward_workspace_bytes", "moe_route_backward", "moe_combine_dropout",
+    "moe_combine_dropout_backward",
     "moe_probe_stream_read",
 )
 MOE_PIPELINE_MAX_DEPTH = 4
@@ -221,6 +224,23 @@ def lib():
     L.moe_priority_order.argtypes = [_P, _I32, _I32, _P, _P, _SZ, _P]
     L.moe_set_stage_events.restype = ctypes.c_int
     L.moe_set_stage_events.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
+    L.moe_balance_loss_workspace_bytes.restype = _SZ
+    L.moe_balance_loss_workspace_bytes.argtypes = [_I32, _I32]
+    L.moe_balance_loss.restype = ctypes.c_int
+    L.moe_balance_loss.argtypes = [_P, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P, _P,
+                                   _P, _SZ, _P]
+    L.moe_route_backward_workspace_bytes.restype = _SZ
+    L.moe_route_backward_workspace_bytes.argtypes = [_I32, _I32, _I32, ctypes.c_int]
+    L.moe_route_backward.restype = ctypes.c_int
+    L.moe_route_backward.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P,
+                                     _I32, _I32, _I32, _I32, ctypes.c_int,
+                                     ctypes.POINTER(moe_options), _P, _P, _P, _P, _SZ, _P]
+    L.moe_combine_dropout.restype = ctypes.c_int
+    L.moe_combine_dropout.argtypes = [_P, _P, _P, _P, _D, _P, _I32, _I32, _I32, ctypes.c_int, _P,
+                                      _P]
+    L.moe_combine_dropout_backward.restype = ctypes.c_int
+    L.moe_combine_dropout_backward.argtypes = [_P, _P, _P, _P, _D, _P, _I32, _I32, _I32,
+                                               ctypes.c_int, _P, _P, _P]
     L.moe_probe_stream_read.restype = ctypes.c_int
     L.moe_probe_stream_read.argtypes = [_P, _SZ, _P, _P]
     _lib_handle = L
@@ -634,10 +654,232 @@ class MoELayer:
                            stream=stream, gating=self.gating, gate_scale=self.gate_scale,
                            priority=self.priority)
 
+    def forward_train(self, x, coef=0.0, mask=None, residual=None, p=0.0, rng=None):
+        """One forward pass that a backward pass can follow, on the current
+        stream: (y, loss, step) with y = residual + dropout_p(layer(x)), the
+        balance loss [1] weighted by coef (mask: see moe_balance_loss), and
+        ``step``, the dict of intermediates that backward_combine and
+        backward_router read (xp, h, o, offsets and kept_counts among them,
+        for a backward pass of the experts).  x, gates and rng are held, not
+        copied."""
+        idx, gate, _ = moe_route(x, self.Wg, self.bias, self.k, gating=self.gating,
+                                 gate_scale=self.gate_scale)
+        scores = moe_expert_choice_route(x, self.Wg, self.bias)
+        balance = moe_balance_loss(scores, idx, coef, mask=mask)
+        order = None
+        if self.priority in ("gate", MOE_PRIORITY_GATE) and moe_capacity(
+                x.shape[0], self.E, self.k, self.cf) >= 0:
+            order = moe_priority_order(gate)
+        perm = moe_permute(x, idx, self.E, self.cf, order=order)
+        h, o, dev_error = moe_grouped_ffn(perm["xp"], perm["offsets"], perm["kept_counts"],
+                                          self.W1, self.W3, self.W2, self.act)
+        y = moe_combine_dropout(o, perm["pos"], gate, p=p, rng=rng, residual=residual)
+        step = dict(x=x, idx=idx, gate=gate, scores=scores, mask=mask, coef=coef, p=p, rng=rng,
+                    balance_counts=balance["counts"], tokens=balance["tokens"], h=h, o=o,
+                    dev_error=dev_error, **perm)
+        return y, balance["loss"], step
+
+    def backward_combine(self, step, dy, d_o=None):
+        """d_o, the gradient of the expert outputs step["o"] (kept rows only);
+        the gates' gradient is left in step["dgate"]."""
+        d_o, step["dgate"] = moe_combine_dropout_backward(dy, step["o"], step["pos"],
+                                                          step["gate"], step["p"], step["rng"],
+                                                          d_o=d_o)
+        return d_o
+
+    def backward_router(self, step, dloss=None, dxp=None, outputs=("dx", "dWg", "dbias")):
+        """The router's gradients after backward_combine, as a dict: through
+        the gates and the balance loss (dloss [1]: its gradient, None for 1).
+        dxp: the gradient of the permuted tokens step["xp"] from the experts'
+        own backward pass; dx then holds both."""
+        dx_acc = None
+        if dxp is not None and "dx" in outputs:
+            dx_acc = moe_unpermute_combine(dxp, step["pos"], torch.ones_like(step["gate"]),
+                                           step["x"].dtype)
+        return moe_route_backward(step["x"], self.Wg, step["idx"], step["gate"], step["dgate"],
+                                  step["scores"], step["balance_counts"], step["tokens"],
+                                  step["coef"], dloss, step["mask"], self.gating, self.gate_scale,
+                                  dx_acc=dx_acc, dx=dx_acc, outputs=outputs)
+
     def graph(self, x, y=None):
         """A ForwardGraph of this layer on x (and y, allocated if None)."""
         y = y if y is not None else torch.empty_like(x)
         return ForwardGraph(self, x, y)
+
+
+# ---------------------------------------------------------------- training
+_MASK_TYPES = (torch.bool, torch.uint8)
+
+
+def _tensor(t, name, dtypes, shape, dev):
+    """The address of an argument that the kernels will read or write: its
+    type, shape, device and dense layout are checked here, because a raw
+    pointer carries none of them.  None passes as NULL."""
+    if t is None:
+        return None
+    if t.dtype is not dtypes and t.dtype not in (dtypes if type(dtypes) is tuple else (dtypes,)):
+        raise TypeError(f"{name} is {t.dtype}, expected {dtypes}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _cuda_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}: the kernels need CUDA tensors")
+    return t.device
+
+
+def _launch(fn, where, dev, stream, *args):
+    """fn(*args, stream) with ``dev`` current (its own stream if none is given)."""
+    s = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    _check(status, where)
+
+
+def _empty(shape, dtype, dev, stream):
+    """A new tensor that belongs to the stream the kernels run on, so that its
+    memory is not handed out again while they use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _workspace(ws, need, dev, stream):
+    if ws is None:
+        return _empty(max(need, 16), torch.uint8, dev, stream)
+    if not ws.is_contiguous() or ws.device != dev:
+        raise ValueError("ws is not a contiguous tensor on the device of the call")
+    return ws
+
+
+def moe_balance_loss_workspace_bytes(T, E):
+    return lib().moe_balance_loss_workspace_bytes(T, E)
+
+
+def moe_balance_loss(scores, idx, coef, mask=None, loss=None, prob_sum=None, counts=None,
+                     tokens=None, ws=None, stream=None):
+    """The router's load-balancing loss and what it is made of.
+
+    scores [E, T] fp32 (moe_expert_choice_route), idx [T, k] int32
+    (moe_route), mask [T] bool or uint8 (False: a padding token, counted
+    nowhere).  Returns loss [1] = coef E sum_e counts_e / (N k) prob_sum_e / N,
+    prob_sum [E] fp32, counts [E] int32 and tokens [1] int32 (N)."""
+    E, T = scores.shape
+    k = idx.shape[1]
+    dev = _cuda_device(scores, "scores")
+    i32, f32 = torch.int32, torch.float32
+    loss = loss if loss is not None else _empty(1, f32, dev, stream)
+    prob_sum = prob_sum if prob_sum is not None else _empty(E, f32, dev, stream)
+    counts = counts if counts is not None else _empty(E, i32, dev, stream)
+    tokens = tokens if tokens is not None else _empty(1, i32, dev, stream)
+    ws = _workspace(ws, 0 if ws is not None else moe_balance_loss_workspace_bytes(T, E), dev,
+                    stream)
+    _launch(lib().moe_balance_loss, "moe_balance_loss", dev, stream,
+            _tensor(scores, "scores", f32, (E, T), dev), _tensor(idx, "idx", i32, (T, k), dev),
+            _tensor(mask, "mask", _MASK_TYPES, (T,), dev), T, E, k, coef,
+            _tensor(loss, "loss", f32, (1,), dev), _tensor(prob_sum, "prob_sum", f32, (E,), dev),
+            _tensor(counts, "counts", i32, (E,), dev), _tensor(tokens, "tokens", i32, (1,), dev),
+            ws.data_ptr(), ws.numel() * ws.element_size())
+    return dict(loss=loss, prob_sum=prob_sum, counts=counts, tokens=tokens)
+
+
+def moe_route_backward_workspace_bytes(T, d, E, dtype):
+    code = MOE_BF16 if dtype in (torch.bfloat16, "bf16") else MOE_FP32
+    return lib().moe_route_backward_workspace_bytes(T, d, E, code)
+
+
+def moe_route_backward(x, Wg, idx, gate=None, dgate=None, scores=None, counts=None, tokens=None,
+                       coef=0.0, dloss=None, mask=None, gating="topk_softmax", gate_scale=1.0,
+                       dx_acc=None, dx=None, dWg=None, dbias=None,
+                       outputs=("dx", "dWg", "dbias"), ws=None, stream=None):
+    """Gradients of x, W_g and the router bias, from dgate [T, k] (the gates'
+    gradient; needs gate) and from the balance loss (counts and tokens as
+    moe_balance_loss returned them, coef, and dloss [1], the gradient of the
+    loss; None for 1) -- either or both.  scores [E, T] serve the loss and
+    the softmax-then-TopK gates.  dx is added to dx_acc where that is given
+    (dx may be dx_acc itself).  ``outputs`` names the gradients to compute;
+    returns them as a dict (dx in the layer dtype, the others fp32)."""
+    T, d = x.shape
+    E = Wg.shape[1]
+    k = idx.shape[1]
+    dev = _cuda_device(x, "x")
+    i32, f32, dt = torch.int32, torch.float32, x.dtype
+    code = _dtype_code(x)
+    out = {}
+    for name, given, shape, dtype in (("dx", dx, (T, d), dt), ("dWg", dWg, (d, E), f32),
+                                      ("dbias", dbias, (E,), f32)):
+        if name in outputs:
+            out[name] = given if given is not None else _empty(shape, dtype, dev, stream)
+    if len(out) != len(outputs):
+        raise ValueError(f"outputs {outputs}: dx, dWg and dbias, each at most once")
+    ws = _workspace(ws, 0 if ws is not None else
+                    moe_route_backward_workspace_bytes(T, d, E, dt), dev, stream)
+    opt = _options(gating, gate_scale)
+    _launch(lib().moe_route_backward, "moe_route_backward", dev, stream,
+            _tensor(x, "x", dt, (T, d), dev), _tensor(Wg, "Wg", dt, (d, E), dev),
+            _tensor(scores, "scores", f32, (E, T), dev), _tensor(idx, "idx", i32, (T, k), dev),
+            _tensor(gate, "gate", f32, (T, k), dev), _tensor(dgate, "dgate", f32, (T, k), dev),
+            _tensor(counts, "counts", i32, (E,), dev), _tensor(tokens, "tokens", i32, (1,), dev),
+            _tensor(dloss, "dloss", f32, (1,), dev), coef,
+            _tensor(mask, "mask", _MASK_TYPES, (T,), dev),
+            _tensor(dx_acc, "dx_acc", dt, (T, d), dev), T, d, E, k, code, ctypes.byref(opt),
+            _tensor(out.get("dx"), "dx", dt, (T, d), dev),
+            _tensor(out.get("dWg"), "dWg", f32, (d, E), dev),
+            _tensor(out.get("dbias"), "dbias", f32, (E,), dev), ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    return out
+
+
+def moe_combine_dropout(o, pos, gate, p=0.0, rng=None, residual=None, y=None, stream=None):
+    """y [T, d] = residual + dropout_p(sum_j gate o[pos]): the combine, dropout
+    of its result and the residual in one pass.  rng: int64 [2] on the device,
+    {seed, offset}, read when the kernel runs; needed unless p rounds to 0.
+    y may be the residual."""
+    T, k = pos.shape
+    rows, d = o.shape
+    dev = _cuda_device(o, "o")
+    dt = o.dtype
+    code = _dtype_code(o)
+    y = y if y is not None else _empty((T, d), dt, dev, stream)
+    _launch(lib().moe_combine_dropout, "moe_combine_dropout", dev, stream,
+            _tensor(o, "o", dt, (rows, d), dev), _tensor(pos, "pos", torch.int32, (T, k), dev),
+            _tensor(gate, "gate", torch.float32, (T, k), dev),
+            _tensor(residual, "residual", dt, (T, d), dev), p,
+            _tensor(rng, "rng", torch.int64, (2,), dev), T, d, k, code,
+            _tensor(y, "y", dt, (T, d), dev))
+    return y
+
+
+def moe_combine_dropout_backward(dy, o, pos, gate, p=0.0, rng=None, d_o=None, dgate=None,
+                                 stream=None):
+    """(d_o [rows, d], dgate [T, k]) of moe_combine_dropout with the same p and
+    rng (p = 0: of moe_unpermute_combine).  Rows of d_o that no kept slot owns
+    are left as they were (uninitialised when d_o is allocated here)."""
+    T, k = pos.shape
+    rows, d = o.shape
+    dev = _cuda_device(o, "o")
+    dt = o.dtype
+    code = _dtype_code(o)
+    d_o = d_o if d_o is not None else _empty((rows, d), dt, dev, stream)
+    dgate = dgate if dgate is not None else _empty((T, k), torch.float32, dev, stream)
+    _launch(lib().moe_combine_dropout_backward, "moe_combine_dropout_backward", dev, stream,
+            _tensor(dy, "dy", dt, (T, d), dev), _tensor(o, "o", dt, (rows, d), dev),
+            _tensor(pos, "pos", torch.int32, (T, k), dev),
+            _tensor(gate, "gate", torch.float32, (T, k), dev), p,
+            _tensor(rng, "rng", torch.int64, (2,), dev), T, d, k, code,
+            _tensor(d_o, "d_o", dt, (rows, d), dev),
+            _tensor(dgate, "dgate", torch.float32, (T, k), dev))
+    return d_o, dgate
 
 
 # ------------------------------------------------ expert-choice routing

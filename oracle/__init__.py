@@ -37,3 +37,13 @@ from .moe_oracle import (  # noqa: F401
     expert_choice_select,
     moe_forward_expert_choice,
 )
+from .moe_training import (  # noqa: F401
+    philox4x32_10,
+    dropout_keep,
+    dropout_threshold,
+    balance_loss,
+    router_dlogits,
+    route_backward,
+    combine_dropout,
+    combine_dropout_backward,
+)
