@@ -13,174 +13,211 @@
 // tokens.  (2) Both products in one pass over x: a CTA owns a block of
 // columns and a range of tokens, so each x element is read once, each dx
 // element written once, and dW_g of the block stays on the chip until the
-// range is done.  (3) The ranges' dW_g and the blocks' column sums added in
-// order (no floating-point atomics).
+// range is done (bf16: tensor cores, route_backward_tc.cu; fp32: FMA, here).
+// (3) The ranges' dW_g and the blocks' column sums added in order (no
+// floating-point atomics).
 
-#include "moe_internal.cuh"
+#include "route_backward.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kRbTokens = 128;    // tokens of one dz block
-constexpr int kRbCols = 64;       // columns of one product CTA
-constexpr int kRbTile = 32;       // tokens of one tile
-constexpr int kRbThreads = 256;
+constexpr int kDzThreads = 4 * kRbTokens;
+constexpr int kCols = 64;          // fp32 products: columns of one CTA,
+constexpr int kTile = 32;          // tokens of one tile
+constexpr int kThreads = 256;
 
-// Experts rounded up to the widths the product kernels are built for.
-int padded_experts(int E) { return E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64; }
+// Token ranges for `cols` column blocks: the number that needs the fewest
+// tile times, where a wave of kRbSms CTAs takes the tiles of its longest
+// range and about two more for its start and its end.
+int pick_ranges(int cols, int tiles, int per_sm) {
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  const int slots = kRbSms * per_sm;
+  const int most = tiles < 2 * slots / cols + 1 ? tiles : 2 * slots / cols + 1;
+  for (int r = 1; r <= most; ++r) {
+    const int64_t waves = (static_cast<int64_t>(cols) * r + slots - 1) / slots;
+    const int64_t cost = waves * ((tiles + r - 1) / r + 2);
+    if (cost < best_cost) best_cost = cost, best = r;
+  }
+  return best;
+}
 
-struct Plan {
-  int EP;           // padded experts: dz is [T, EP], zero past E
-  int blocks;       // dz blocks
-  int cols;         // column blocks
-  int ranges;       // token ranges
-  int range;        // tokens of a range (a multiple of kRbTile)
-  size_t dz, bias, dw, total;  // byte offsets in the workspace
-};
-
-Plan make_plan(int T, int d, int E) {
-  Plan p;
-  p.EP = padded_experts(E);
+RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
+  RouteBackwardPlan p{};
+  const bool tc = dtype == MOE_BF16;
+  p.EP = E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64;
   p.blocks = (T + kRbTokens - 1) / kRbTokens;
-  p.cols = (d + kRbCols - 1) / kRbCols;
-  const int tiles = (T + kRbTile - 1) / kRbTile;
-  int want = (148 * 4 + p.cols - 1) / p.cols;
-  if (want > tiles) want = tiles;
-  if (want < 1) want = 1;
-  p.range = (tiles + want - 1) / want * kRbTile;
-  p.ranges = p.range ? (T + p.range - 1) / p.range : 0;
+  const int cols = tc ? kRbTcCols : kCols, tile = tc ? kRbTcTokens : kTile;
+  p.cols = (d + cols - 1) / cols;
+  p.tiles = (T + tile - 1) / tile;
+  p.ranges = T > 0 ? pick_ranges(p.cols, p.tiles, tc ? 1 : 4) : 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at = (at + bytes + 255) / 256 * 256;
     return here;
   };
-  p.dz = take(sizeof(float) * p.EP * static_cast<size_t>(T));
-  p.bias = take(sizeof(float) * kMaxE * static_cast<size_t>(p.blocks));
-  p.dw = take(sizeof(float) * d * static_cast<size_t>(E) * p.ranges);
+  p.err = take(sizeof(int32_t));
+  const size_t row = tc ? 128 * dz_terms(E).blocks : sizeof(float) * p.EP;
+  p.dz = take(row * T);
+  p.bias = take(sizeof(float) * kMaxE * p.blocks);
+  p.dw = take(sizeof(float) * d * E * p.ranges);
   p.total = at;
   return p;
 }
 
-// One thread a token: its row of dz, through shared memory so that the block
-// writes whole rows, and the block's column sums.
-__global__ void __launch_bounds__(kRbTokens)
-    route_dz_kernel(RouteBackwardArgs a, int EP, float* __restrict__ dz,
-                    float* __restrict__ bias_part) {
-  extern __shared__ float row_s[];  // [EP][kRbTokens]
+__device__ __forceinline__ float bf16_round(float v) {
+  return __bfloat162float(__float2bfloat16(v));
+}
+
+// dz of 64 tokens, four threads a token (each a quarter of the experts, kept
+// in registers so that the scores are read once), and its column sums.  TC:
+// dz leaves as bf16 terms, else as fp32 rows of EP.
+template <bool TC>
+__global__ void __launch_bounds__(kDzThreads)
+    route_dz_kernel(const RouteBackwardArgs a, int EP, DzTerms terms, void* __restrict__ dz,
+                    float* __restrict__ bias_part, int32_t* __restrict__ err) {
+  __shared__ float z[kRbTokens][kMaxE + 1];
   __shared__ float f[kMaxE];
+  __shared__ float part[2][4][kRbTokens];
+  const int tid = threadIdx.x, tok = tid % kRbTokens, q = tid / kRbTokens;
+  const int t0 = blockIdx.x * kRbTokens, t = t0 + tok;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
-  const int t = blockIdx.x * kRbTokens + tid;
-  float c = 0.f;
-  if (a.counts) {
-    const int n = *a.tokens;
-    if (n > 0) {
-      c = a.coef * (a.dloss ? *a.dloss : 1.f) * a.E / n;
-      if (tid < a.E) f[tid] = static_cast<float>(a.counts[tid]) / (static_cast<float>(n) * a.k);
-    } else if (tid < a.E) {
-      f[tid] = 0.f;
+  if (blockIdx.x == 0 && tid == 0) *err = 0;
+  const int n = a.counts ? *a.tokens : 0;
+  if (tid < kMaxE)
+    f[tid] = n > 0 && tid < a.E
+                 ? static_cast<float>(a.counts[tid]) / (static_cast<float>(n) * a.k)
+                 : 0.f;
+  const float c = n > 0 ? a.coef * (a.dloss ? *a.dloss : 1.f) * a.E / n : 0.f;
+  const bool live = t < a.T && (!a.mask || a.mask[t]);
+  const bool all = a.dgate && a.gating == MOE_GATE_SOFTMAX_TOPK;
+  const bool loss = n > 0;
+  float p[kMaxE / 4];
+#pragma unroll
+  for (int i = 0; i < kMaxE / 4; ++i) {
+    const int e = q + 4 * i;
+    p[i] = live && (loss || all) && e < a.E ? a.scores[static_cast<int64_t>(e) * a.T + t] : 0.f;
+  }
+  const int64_t slot = static_cast<int64_t>(t) * a.k;
+  float total = 0.f, mean = 0.f;
+  if (live && a.dgate)
+    for (int j = q; j < a.k; j += 4) total = fmaf(a.gate[slot + j], a.dgate[slot + j], total);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kMaxE / 4; ++i)
+    if (q + 4 * i < a.E) mean = fmaf(f[q + 4 * i], p[i], mean);
+  part[0][q][tok] = total;
+  part[1][q][tok] = mean;
+  __syncthreads();
+  total = (part[0][0][tok] + part[0][1][tok]) + (part[0][2][tok] + part[0][3][tok]);
+  mean = (part[1][0][tok] + part[1][1][tok]) + (part[1][2][tok] + part[1][3][tok]);
+#pragma unroll
+  for (int i = 0; i < kMaxE / 4; ++i) {
+    const int e = q + 4 * i;
+    float v = 0.f;
+    if (live && loss) v = c * p[i] * (f[e] - mean);
+    if (live && all) v -= p[i] * total;
+    z[tok][e] = v;
+  }
+  __syncthreads();
+  // One thread a token, slot after slot: the same expert may come twice.
+  if (q == 0 && live && a.dgate)
+    for (int j = 0; j < a.k; ++j) {
+      const int e = a.idx[slot + j];
+      if (e < 0 || e >= a.E) continue;
+      const float g = a.gate[slot + j], dg = a.dgate[slot + j];
+      z[tok][e] += all ? g * dg : g * (dg - total / a.gate_scale);
     }
-  }
-  for (int e = 0; e < EP; ++e) row_s[e * kRbTokens + tid] = 0.f;
   __syncthreads();
-  if (t < a.T && (!a.mask || a.mask[t])) {
-    float total = 0.f, mean = 0.f;
-    if (a.dgate)
-      for (int j = 0; j < a.k; ++j)
-        total = fmaf(a.gate[static_cast<int64_t>(t) * a.k + j],
-                     a.dgate[static_cast<int64_t>(t) * a.k + j], total);
-    if (a.counts)
-      for (int e = 0; e < a.E; ++e)
-        mean = fmaf(f[e], a.scores[static_cast<int64_t>(e) * a.T + t], mean);
-    const bool all = a.dgate && a.gating == MOE_GATE_SOFTMAX_TOPK;
-    if (a.counts || all)
-      for (int e = 0; e < a.E; ++e) {
-        const float p = a.scores[static_cast<int64_t>(e) * a.T + t];
-        row_s[e * kRbTokens + tid] = (a.counts ? c * p * (f[e] - mean) : 0.f) - (all ? p * total : 0.f);
+  const int rows = min(kRbTokens, a.T - t0);
+  if (TC) {
+    const int chunks = 8 * terms.blocks;  // 16-byte chunks of a row
+    uint4* out = static_cast<uint4*>(dz) + static_cast<int64_t>(t0) * chunks;
+    for (int i = tid; i < rows * chunks; i += kDzThreads) {
+      const int r = i / chunks, ch = i % chunks;
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int m = ch * 8 + u, term = m / terms.stride, e = m % terms.stride;
+        float w = term < 3 ? z[r][e] : 0.f;  // columns past E are zero
+        const float hi = bf16_round(w);
+        if (term > 0) w = isfinite(hi) ? w - hi : 0.f;
+        if (term > 1) w -= bf16_round(w);
+        v[u] = w;
       }
-    if (a.dgate)
-      for (int j = 0; j < a.k; ++j) {
-        const int e = a.idx[static_cast<int64_t>(t) * a.k + j];
-        if (e < 0 || e >= a.E) continue;
-        const float g = a.gate[static_cast<int64_t>(t) * a.k + j];
-        const float dg = a.dgate[static_cast<int64_t>(t) * a.k + j];
-        row_s[e * kRbTokens + tid] += all ? g * dg : g * (dg - total / a.gate_scale);
-      }
+      out[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+  } else {
+    float* out = static_cast<float*>(dz) + static_cast<int64_t>(t0) * EP;
+    for (int i = tid; i < rows * EP; i += kDzThreads) out[i] = z[i / EP][i % EP];
   }
+  // tok is an expert here, q a quarter of the tokens.
+  float s = 0.f;
+  for (int r = 0; r < kRbTokens / 4; ++r) s += z[q * (kRbTokens / 4) + r][tok];
+  part[0][q][tok] = s;
   __syncthreads();
-  const int rows = min(kRbTokens, a.T - static_cast<int>(blockIdx.x) * kRbTokens);
-  float* out = dz + static_cast<int64_t>(blockIdx.x) * kRbTokens * EP;
-  for (int i = tid; i < rows * EP; i += kRbTokens) out[i] = row_s[(i % EP) * kRbTokens + i / EP];
-  if (tid < a.E) {
-    float s = 0.f;
-    for (int i = 0; i < rows; ++i) s += row_s[tid * kRbTokens + i];
-    bias_part[static_cast<int64_t>(blockIdx.x) * kMaxE + tid] = s;
-  }
+  if (q == 0)
+    bias_part[static_cast<int64_t>(blockIdx.x) * kMaxE + tok] =
+        (part[0][0][tok] + part[0][1][tok]) + (part[0][2][tok] + part[0][3][tok]);
 }
 
-template <bool BF16>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if (BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
-  return reinterpret_cast<const float*>(p)[i];
-}
-template <bool BF16>
-__device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-  if (BF16)
-    reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16(v);
-  else
-    reinterpret_cast<float*>(p)[i] = v;
-}
-
-// Both products on fp32 FMA: thread (column, quarter) keeps its column's
-// share of dW_g (a quarter of the experts) and its column of W_g in
-// registers, and makes dx for a quarter of the tile's tokens.
-template <bool BF16, int EP>
-__global__ void __launch_bounds__(kRbThreads)
-    route_products_kernel(RouteBackwardArgs a, int range, const float* __restrict__ dz,
-                          float* __restrict__ dw) {
+// Both products of an fp32 layer, on fp32 FMA: thread (column, quarter) keeps
+// its column's share of dW_g (a quarter of the experts) and its column of W_g
+// in registers, and makes dx for a quarter of the tile's tokens.
+template <int EP>
+__global__ void __launch_bounds__(kThreads)
+    route_products_kernel(const RouteBackwardArgs a, int ranges, int tiles,
+                          const float* __restrict__ dz, float* __restrict__ dw) {
   constexpr int QE = EP / 4;
-  __shared__ __align__(16) float dz_s[kRbTile][EP];
-  __shared__ float x_s[kRbTile][kRbCols];
-  const int tid = threadIdx.x, col = tid % kRbCols, q = tid / kRbCols;
-  const int c = blockIdx.x * kRbCols + col;
+  __shared__ __align__(16) float dz_s[kTile][EP];
+  __shared__ float x_s[kTile][kCols];
+  const float* x = static_cast<const float*>(a.x);
+  const float* Wg = static_cast<const float*>(a.Wg);
+  const float* dx_acc = static_cast<const float*>(a.dx_acc);
+  float* dx = static_cast<float*>(a.dx);
+  const int tid = threadIdx.x, col = tid % kCols, q = tid / kCols;
+  const int c = blockIdx.x * kCols + col;
   const bool in = c < a.d;
   pdl_wait();
   pdl_trigger();
   float w[EP], acc[QE];
 #pragma unroll
   for (int e = 0; e < EP; ++e)
-    w[e] = a.dx && in && e < a.E ? load1<BF16>(a.Wg, static_cast<int64_t>(c) * a.E + e) : 0.f;
+    w[e] = dx && in && e < a.E ? Wg[static_cast<int64_t>(c) * a.E + e] : 0.f;
 #pragma unroll
   for (int e = 0; e < QE; ++e) acc[e] = 0.f;
-  const int t0 = blockIdx.y * range, t1 = min(a.T, t0 + range);
-  for (int tb = t0; tb < t1; tb += kRbTile) {
+  const int t0 = static_cast<int>(static_cast<int64_t>(blockIdx.y) * tiles / ranges) * kTile;
+  const int t1 = min(a.T, static_cast<int>(static_cast<int64_t>(blockIdx.y + 1) * tiles / ranges) *
+                              kTile);
+  for (int tb = t0; tb < t1; tb += kTile) {
     __syncthreads();
-    const int rows = min(kRbTile, t1 - tb);
-    for (int i = tid; i < kRbTile * EP; i += kRbThreads)
+    const int rows = min(kTile, t1 - tb);
+    for (int i = tid; i < kTile * EP; i += kThreads)
       (&dz_s[0][0])[i] = i < rows * EP ? dz[static_cast<int64_t>(tb) * EP + i] : 0.f;
     if (a.dWg)
-      for (int r = q; r < kRbTile; r += 4) {
+      for (int r = q; r < kTile; r += 4) {
         const int t = tb + r;
         const bool use = in && r < rows && (!a.mask || a.mask[t]);
-        x_s[r][col] = use ? load1<BF16>(a.x, static_cast<int64_t>(t) * a.d + c) : 0.f;
+        x_s[r][col] = use ? x[static_cast<int64_t>(t) * a.d + c] : 0.f;
       }
     __syncthreads();
     if (a.dWg)
-      for (int r = 0; r < kRbTile; ++r) {
+      for (int r = 0; r < kTile; ++r) {
         const float xv = x_s[r][col];
 #pragma unroll
         for (int e = 0; e < QE; ++e) acc[e] = fmaf(xv, dz_s[r][q * QE + e], acc[e]);
       }
-    if (a.dx && in)
+    if (dx && in)
       for (int r = q; r < rows; r += 4) {
         const int64_t at = static_cast<int64_t>(tb + r) * a.d + c;
         float v = 0.f;
 #pragma unroll
         for (int e = 0; e < EP; ++e) v = fmaf(dz_s[r][e], w[e], v);
-        if (a.dx_acc) v += load1<BF16>(a.dx_acc, at);
-        store1<BF16>(a.dx, at, v);
+        dx[at] = dx_acc ? v + dx_acc[at] : v;
       }
   }
   if (a.dWg && in)
@@ -190,67 +227,90 @@ __global__ void __launch_bounds__(kRbThreads)
         dw[(static_cast<int64_t>(blockIdx.y) * a.d + c) * a.E + q * QE + e] = acc[e];
 }
 
-__global__ void __launch_bounds__(256)
+// The ranges' dW_g (CTAs 0 .. dw_ctas - 1, four elements a thread) and the
+// blocks' column sums (one CTA an expert), each in a fixed order.  After a
+// time-out in the products nothing here is right: NaN says so.
+__global__ void __launch_bounds__(kThreads)
     route_finish_kernel(const float* __restrict__ dw, const float* __restrict__ bias_part,
-                        int ranges, int blocks, int64_t n, int E, float* __restrict__ dWg,
-                        float* __restrict__ dbias) {
+                        const int32_t* __restrict__ err, int ranges, int blocks, int64_t n,
+                        int dw_ctas, float* __restrict__ dWg, float* __restrict__ dbias) {
+  __shared__ float warp_sum[kThreads / 32];
+  const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (dWg && i < n) {
-    float s = 0.f;
-    for (int r = 0; r < ranges; ++r) s += dw[r * n + i];
-    dWg[i] = s;
+  const bool failed = ranges > 0 && *err != 0;
+  if (static_cast<int>(blockIdx.x) < dw_ctas) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + tid) * 4;
+    if (i >= n) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int r = 0; r < ranges; ++r) {
+      const float4 v = *reinterpret_cast<const float4*>(dw + r * n + i);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    if (failed) s.x = s.y = s.z = s.w = __int_as_float(0x7fc00000);
+    *reinterpret_cast<float4*>(dWg + i) = s;
+    return;
   }
-  if (dbias && i < E) {
-    float s = 0.f;
-    for (int b = 0; b < blocks; ++b) s += bias_part[static_cast<int64_t>(b) * kMaxE + i];
-    dbias[i] = s;
+  const int e = blockIdx.x - dw_ctas;
+  float s = 0.f;
+  for (int b = tid; b < blocks; b += kThreads) s += bias_part[static_cast<int64_t>(b) * kMaxE + e];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (tid % 32 == 0) warp_sum[tid / 32] = s;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kThreads / 32; ++w) s += warp_sum[w];
+    dbias[e] = s;
   }
 }
 
-template <bool BF16>
-cudaError_t launch_products(const RouteBackwardArgs& a, const Plan& p, const float* dz, float* dw,
-                            cudaStream_t s) {
+cudaError_t launch_products(const RouteBackwardArgs& a, const RouteBackwardPlan& p,
+                            const float* dz, float* dw, cudaStream_t s) {
   auto go = [&](auto kern) {
-    return launch_kernel(kern, dim3(p.cols, p.ranges), dim3(kRbThreads), 0, s, 1, true, a, p.range,
-                         dz, dw);
+    return launch_kernel(kern, dim3(p.cols, p.ranges), dim3(kThreads), 0, s, 1, true, a, p.ranges,
+                         p.tiles, dz, dw);
   };
   switch (p.EP) {
-    case 8: return go(route_products_kernel<BF16, 8>);
-    case 16: return go(route_products_kernel<BF16, 16>);
-    case 32: return go(route_products_kernel<BF16, 32>);
-    default: return go(route_products_kernel<BF16, 64>);
+    case 8: return go(route_products_kernel<8>);
+    case 16: return go(route_products_kernel<16>);
+    case 32: return go(route_products_kernel<32>);
+    default: return go(route_products_kernel<64>);
   }
 }
 
 }  // namespace
 
-size_t route_backward_scratch_bytes(int T, int d, int E, moe_dtype) {
-  return make_plan(T, d, E).total;
+size_t route_backward_scratch_bytes(int T, int d, int E, moe_dtype dtype) {
+  return make_plan(T, d, E, dtype).total;
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, moe_dtype dtype, cudaStream_t s) {
-  const Plan p = make_plan(a.T, a.d, a.E);
+  const RouteBackwardPlan p = make_plan(a.T, a.d, a.E, dtype);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  float* dz = reinterpret_cast<float*>(ws + p.dz);
+  int32_t* err_word = reinterpret_cast<int32_t*>(ws + p.err);
   float* bias_part = reinterpret_cast<float*>(ws + p.bias);
   float* dw = reinterpret_cast<float*>(ws + p.dw);
   cudaError_t err = cudaSuccess;
   if (a.T > 0) {
-    err = launch_kernel(route_dz_kernel, dim3(p.blocks), dim3(kRbTokens),
-                        sizeof(float) * p.EP * kRbTokens, s, 1, true, a, p.EP, dz, bias_part);
+    auto dz = [&](auto kern) {
+      return launch_kernel(kern, dim3(p.blocks), dim3(kDzThreads), 0, s, 1, true, a, p.EP,
+                           dz_terms(a.E), static_cast<void*>(ws + p.dz), bias_part, err_word);
+    };
+    const bool tc = dtype == MOE_BF16;
+    err = tc ? dz(route_dz_kernel<true>) : dz(route_dz_kernel<false>);
     if (err == cudaSuccess && (a.dx || a.dWg))
-      err = dtype == MOE_BF16 ? launch_products<true>(a, p, dz, dw, s)
-                              : launch_products<false>(a, p, dz, dw, s);
+      err = tc ? launch_route_products_tc(a, p, s)
+               : launch_products(a, p, reinterpret_cast<const float*>(ws + p.dz), dw, s);
     if (err != cudaSuccess) return err;
   }
   if (!a.dWg && !a.dbias) return cudaSuccess;
   const int64_t n = static_cast<int64_t>(a.d) * a.E;
-  return launch_kernel(route_finish_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256),
-                       0, s, 1, true, static_cast<const float*>(dw),
-                       static_cast<const float*>(bias_part), p.ranges, p.blocks, n, a.E, a.dWg,
-                       a.dbias);
+  const int dw_ctas = a.dWg ? static_cast<int>((n / 4 + kThreads - 1) / kThreads) : 0;
+  return launch_kernel(route_finish_kernel, dim3(dw_ctas + (a.dbias ? a.E : 0)), dim3(kThreads), 0,
+                       s, 1, true, static_cast<const float*>(dw),
+                       static_cast<const float*>(bias_part), static_cast<const int32_t*>(err_word),
+                       p.ranges, p.blocks, n, dw_ctas, a.dWg, a.dbias);
 }
 
 }  // namespace moe

@@ -1,0 +1,435 @@
+// The two products of the router's backward pass for bf16 layers, on the
+// tensor cores, in one pass over x:
+//
+//     dW_g = x^T dz   (M = 128 columns, N = experts x terms, K = tokens)
+//     dx = dx_acc + dz W_g^T   (M = 128 tokens, N = 128 columns, K = experts)
+//
+// A CTA owns 128 columns and a range of tokens, in tiles of 128 tokens.  Per
+// tile TMA brings 128 x 128 of x and the tokens' dz terms (route_backward.cuh)
+// into one stage of a ring; the same dz bytes are the N-major operand of the
+// first product and the K-major operand of the second.  dW_g accumulates in
+// tensor memory over the whole range; dx of a tile goes through one of two
+// accumulators to the epilogue warps, which add dx_acc (brought by TMA into
+// the buffer that the result leaves from), round once and store by TMA.
+// Bound by HBM: x is read once and dx written once; dz is re-read from L2 by
+// every column block.
+//
+// Warps: 0 TMA loads, 1 MMA issue, 2-3 zero the rows of padding tokens in x
+// (with a mask only: their x may hold anything, and 0 * NaN is NaN), 4-7
+// epilogue.  Every wait is bounded; a time-out raises the workspace's error
+// word and the CTA leaves after its copies and MMAs have landed.
+
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "route_backward.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnit = 128 * 64 * 2;   // 64 columns (or experts) of 128 rows: 16 KB
+constexpr int kMaxStages = 3;
+constexpr int kMaxUnits = 4;
+constexpr int kDwCol = 256;           // dW_g's first column in tensor memory
+constexpr int kSmem = 14 * kUnit + 2048;  // + control block and alignment
+
+// NB: 64-element blocks of a dz row.  Stages x (2 + NB), W_g blocks and
+// staging units add up to the same 14 blocks of shared memory.
+template <int NB>
+struct Cfg {
+  static constexpr int STAGES = NB == 1 ? 3 : 2;
+  static constexpr int WB = NB == 3 ? 1 : NB;
+  static constexpr int UNITS = NB == 3 ? 3 : 4;
+  static constexpr int STAGE = (2 + NB) * kUnit;
+  static constexpr int W_OFF = STAGES * STAGE;
+  static constexpr int OUT_OFF = W_OFF + WB * kUnit;
+  static constexpr int CTL_OFF = OUT_OFF + UNITS * kUnit;
+  static constexpr int KB = NB == 3 ? 2 : NB;  // blocks of dz in dx: hi and mid suffice
+};
+static_assert(Cfg<1>::CTL_OFF == 14 * kUnit && Cfg<2>::CTL_OFF == 14 * kUnit &&
+              Cfg<3>::CTL_OFF == 14 * kUnit, "one shared-memory size");
+
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages], ready[kMaxStages];
+  uint64_t tfull[2], tempty[2];
+  uint64_t accfull[kMaxUnits];
+  uint64_t wready, drain;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+};
+
+struct Params {
+  const __nv_bfloat16* Wg;
+  const uint8_t* mask;
+  float* dw;       // [ranges, d, E]
+  int32_t* err;
+  int T, d, E, stride, cols, ranges, tiles;
+  int want_dx, want_dw, add;
+};
+
+__device__ __forceinline__ void give_up(const Params& p, Ctl& c, int code) {
+  if (!c.abort_flag) atomicOr(p.err, code);
+  c.abort_flag = 1;
+}
+
+// Byte offset of 16-byte chunk `ch` of row r in a 128-byte-swizzled block.
+__device__ __forceinline__ uint32_t swz(int r, int ch) {
+  return static_cast<uint32_t>(r * 128 + ((ch ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The same, and whether all 128 threads say so: one answer for all of them.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, 1, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return all != 0;
+}
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+    route_products_tc_kernel(const __grid_constant__ CUtensorMap tmX,
+                             const __grid_constant__ CUtensorMap tmDz,
+                             const __grid_constant__ CUtensorMap tmAcc,
+                             const __grid_constant__ CUtensorMap tmDx, const Params p) {
+  using C = Cfg<NB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Ctl& c = *reinterpret_cast<Ctl*>(smem + C::CTL_OFF);
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c0 = static_cast<int>(blockIdx.x % p.cols) * kRbTcCols;
+  const int range = blockIdx.x / p.cols;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(range) * p.tiles / p.ranges);
+  const int ntiles =
+      static_cast<int>(static_cast<int64_t>(range + 1) * p.tiles / p.ranges) - tile0;
+  const int halves = c0 + 64 < p.d ? 2 : 1;  // 64-column halves that exist
+
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(smem_u32(&c.full[i]), 1);
+      mbar_init(smem_u32(&c.empty[i]), 1);
+      mbar_init(smem_u32(&c.ready[i]), 64);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&c.tfull[i]), 1);
+      mbar_init(smem_u32(&c.tempty[i]), 4);
+    }
+    for (int i = 0; i < C::UNITS; ++i) mbar_init(smem_u32(&c.accfull[i]), 1);
+    mbar_init(smem_u32(&c.wready), kThreads - 64);
+    mbar_init(smem_u32(&c.drain), 1);
+    c.abort_flag = 0;
+    fence_mbar_init();
+    fence_async_shared();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&c.tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem_base;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------ TMA loads
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      for (int i = 0; i < ntiles; ++i) {
+        if (c.abort_flag || !mbar_wait(smem_u32(&c.empty[stage]), phase ^ 1)) {
+          give_up(p, c, kErrTimeoutProducer);
+          break;
+        }
+        const uint32_t bar = smem_u32(&c.full[stage]);
+        const uint32_t dst = base + stage * C::STAGE;
+        const int row = (tile0 + i) * kRbTcTokens;
+        const int nx = p.want_dw ? halves : 0;
+        mbar_arrive_expect_tx(bar, (nx + NB) * kUnit);
+        for (int h = 0; h < nx; ++h) tma_load_2d(dst + h * kUnit, &tmX, bar, c0 + 64 * h, row);
+        for (int b = 0; b < NB; ++b) tma_load_2d(dst + (2 + b) * kUnit, &tmDz, bar, 64 * b, row);
+        ++issued;
+        if (++stage == C::STAGES) stage = 0, phase ^= 1;
+      }
+      // Nothing may land after the CTA has left: stage s was filled
+      // (issued - 1 - s) / STAGES + 1 times.
+      for (int s = 0; s < C::STAGES && s < issued; ++s)
+        if (!mbar_wait(smem_u32(&c.full[s]), ((issued - 1 - s) / C::STAGES) & 1u))
+          give_up(p, c, kErrTimeoutDrain);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------ MMA issue
+      constexpr uint32_t idesc_dw = idesc_bf16_f32(128, 64 * NB, true, true);
+      constexpr uint32_t idesc_dx = idesc_bf16_f32(128, 128, false, false);
+      const uint64_t wdesc = smem_desc_sw128(base + C::W_OFF, 16, 1024);
+      bool ok = mbar_wait(smem_u32(&c.wready), 0);
+      if (!ok) give_up(p, c, kErrTimeoutMma);
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int i = 0; ok && i < ntiles; ++i) {
+        const int buf = i & 1;
+        ok = !c.abort_flag &&
+             mbar_wait(smem_u32(p.mask ? &c.ready[stage] : &c.full[stage]), phase) &&
+             (!p.want_dx || mbar_wait(smem_u32(&c.tempty[buf]), ((i >> 1) & 1) ^ 1));
+        if (!ok) {
+          give_up(p, c, kErrTimeoutMma);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t src = base + stage * C::STAGE;
+        if (p.want_dx) {
+          // 16 experts are 32 bytes of a 128-byte row.
+          const uint64_t adesc = smem_desc_sw128(src + 2 * kUnit, 16, 1024);
+#pragma unroll
+          for (int b = 0; b < C::KB; ++b)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_bf16(tmem + buf * 128,
+                          adesc + static_cast<uint64_t>((b * kUnit + kk * 32) >> 4),
+                          wdesc + static_cast<uint64_t>(((b % C::WB) * kUnit + kk * 32) >> 4),
+                          idesc_dx, (b > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(smem_u32(&c.tfull[buf]));
+        }
+        if (p.want_dw) {
+          // 16 tokens are 16 rows of 128 bytes; 64-wide blocks lie 16 KB apart.
+          const uint64_t adesc = smem_desc_sw128(src, kUnit, 1024);
+          const uint64_t bdesc = smem_desc_sw128(src + 2 * kUnit, kUnit, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kRbTcTokens / 16; ++kk)
+            tc_mma_bf16(tmem + kDwCol, adesc + static_cast<uint64_t>((kk * 2048) >> 4),
+                        bdesc + static_cast<uint64_t>((kk * 2048) >> 4), idesc_dw,
+                        (i > 0 || kk > 0) ? 1u : 0u);
+        }
+        tc_commit(smem_u32(&c.empty[stage]));
+        if (++stage == C::STAGES) stage = 0, phase ^= 1;
+      }
+      tc_commit(smem_u32(&c.drain));
+      if (!mbar_wait(smem_u32(&c.drain), 0)) give_up(p, c, kErrTimeoutDrain);
+    }
+  } else {
+    // W_g of the block as the K-major operand, term after term, zero past the
+    // last expert and column.
+    for (int i = tid - 64; i < C::WB * 128 * 64; i += kThreads - 64) {
+      const int b = i / (128 * 64), r = i / 64 % 128, j = i % 64;
+      const int n = 64 * b + j, e = NB == 3 ? n : n % p.stride;
+      const bool in = c0 + r < p.d && e < p.E && n < (NB == 3 ? p.E : 3 * p.stride);
+      const __nv_bfloat16 w = in && p.want_dx ? p.Wg[static_cast<int64_t>(c0 + r) * p.E + e]
+                                              : __float2bfloat16(0.f);
+      *reinterpret_cast<__nv_bfloat16*>(smem + C::W_OFF + b * kUnit + swz(r, j / 8) + j % 8 * 2) = w;
+    }
+    fence_async_shared();
+    mbar_arrive(smem_u32(&c.wready));
+    if (warp < 4) {
+      // ------------------------------------------- rows of padding tokens
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int i = 0; p.mask && i < ntiles; ++i) {
+        if (c.abort_flag || !mbar_wait(smem_u32(&c.full[stage]), phase)) {
+          give_up(p, c, kErrTimeoutMma);
+          break;
+        }
+        for (int r = tid - 64; r < kRbTcTokens; r += 64) {
+          const int t = (tile0 + i) * kRbTcTokens + r;
+          if (!p.want_dw || t >= p.T || p.mask[t]) continue;
+          for (int h = 0; h < halves; ++h)
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)
+              *reinterpret_cast<uint4*>(smem + stage * C::STAGE + h * kUnit + r * 128 + ch * 16) =
+                  make_uint4(0, 0, 0, 0);
+        }
+        fence_async_shared();
+        mbar_arrive(smem_u32(&c.ready[stage]));
+        if (++stage == C::STAGES) stage = 0, phase ^= 1;
+      }
+    } else {
+      // ------------------------------------------------------- epilogue
+      const int q = warp - 4, row = q * 32 + lane;
+      const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+      const bool leader = tid == 128;
+      if (p.want_dx) {
+        const int units = ntiles * halves;
+        auto load_acc = [&](int u) {  // dx_acc of unit u into its staging block
+          const uint32_t bar = smem_u32(&c.accfull[u % C::UNITS]);
+          mbar_arrive_expect_tx(bar, kUnit);
+          tma_load_2d(base + C::OUT_OFF + (u % C::UNITS) * kUnit, &tmAcc, bar,
+                      c0 + 64 * (u % halves), (tile0 + u / halves) * kRbTcTokens);
+        };
+        int loaded = 0;
+        if (p.add && leader)
+          for (; loaded < C::UNITS && loaded < units; ++loaded) load_acc(loaded);
+        int done = 0;
+        for (int u = 0; u < units; ++u) {
+          const int i = u / halves, h = u % halves, buf = i & 1, slot = u % C::UNITS;
+          bool ok = !c.abort_flag;
+          if (ok && h == 0) ok = mbar_wait(smem_u32(&c.tfull[buf]), (i >> 1) & 1);
+          if (ok && p.add) ok = mbar_wait(smem_u32(&c.accfull[slot]), (u / C::UNITS) & 1);
+          if (!ok) give_up(p, c, kErrTimeoutEpilogue);
+          if (!epilogue_all(ok)) break;
+          tc_fence_after();
+          float v[2][32];
+          const uint32_t src = tmem + lane_base + buf * 128 + h * 64;
+          tc_ld_32cols(src, v[0]);
+          tc_ld_32cols(src + 32, v[1]);
+          tc_wait_ld();
+          if (h == halves - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.tempty[buf]));
+          }
+          uint8_t* out = smem + C::OUT_OFF + slot * kUnit;
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            uint4* at = reinterpret_cast<uint4*>(out + swz(row, ch));
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = v[ch / 4][ch % 4 * 8 + e];
+            if (p.add) {
+              const uint4 a = *at;
+              const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                f[2 * e] += __uint_as_float(w[e] << 16);
+                f[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+              }
+            }
+            uint4 o;
+            o.x = pack_bf16x2(f[0], f[1]);
+            o.y = pack_bf16x2(f[2], f[3]);
+            o.z = pack_bf16x2(f[4], f[5]);
+            o.w = pack_bf16x2(f[6], f[7]);
+            *at = o;
+          }
+          fence_async_shared();
+          epilogue_sync();
+          ++done;
+          if (leader) {
+            tma_store_2d(&tmDx, base + C::OUT_OFF + slot * kUnit, c0 + 64 * h,
+                         (tile0 + i) * kRbTcTokens);
+            bulk_commit();
+            // Unit u - 1 has left its block: its place is free for unit
+            // u - 1 + UNITS, and, with three blocks or more, the block of
+            // unit u + 2 is free before any thread gets there.
+            bulk_wait_read<1>();
+            if (p.add && u >= 1 && loaded < units) load_acc(loaded++);
+          }
+        }
+        if (leader) {
+          bulk_wait<0>();
+          // Loads that no iteration waited for (only after a time-out).
+          for (int u = done; u < loaded; ++u)
+            mbar_wait(smem_u32(&c.accfull[u % C::UNITS]), (u / C::UNITS) & 1);
+        }
+      }
+      if (p.want_dw) {
+        // dW_g: lane = column.  The terms of one expert lie `stride` apart, so
+        // they are added through shared memory (the ring is idle by now).
+        bool ok = !c.abort_flag && mbar_wait(smem_u32(&c.drain), 0);
+        if (!ok) give_up(p, c, kErrTimeoutEpilogue);
+        if (epilogue_all(ok)) {
+          tc_fence_after();
+          float* rows = reinterpret_cast<float*>(smem);
+          constexpr int LD = 64 * NB + 1;
+          for (int b = 0; b < 2 * NB; ++b) {
+            float v[32];
+            tc_ld_32cols(tmem + lane_base + kDwCol + b * 32, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) rows[row * LD + b * 32 + e] = v[e];
+          }
+          epilogue_sync();
+          const int n = min(kRbTcCols, p.d - c0) * p.E;
+          float* out = p.dw + (static_cast<int64_t>(range) * p.d + c0) * p.E;
+          for (int i = tid - 128; i < n; i += 128) {
+            const float* r = rows + (i / p.E) * LD + i % p.E;
+            out[i] = r[2 * p.stride] + r[p.stride] + r[0];
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// bf16 [rows, cols], boxes of 64 columns x 128 rows, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* at, uint64_t rows, uint64_t cols) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * 2};
+  cuuint32_t box[2] = {64, 128};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(at), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_route_products_tc(const RouteBackwardArgs& a, const RouteBackwardPlan& p,
+                                     cudaStream_t s) {
+  const DzTerms t = dz_terms(a.E);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  CUtensorMap mx, mdz, macc, mdx;
+  // A map that the call does not use is a copy of dz's.
+  if (!make_map(&mdz, ws + p.dz, a.T, 64 * t.blocks)) return cudaErrorInvalidValue;
+  mx = macc = mdx = mdz;
+  if ((a.dWg && !make_map(&mx, a.x, a.T, a.d)) || (a.dx && !make_map(&mdx, a.dx, a.T, a.d)) ||
+      (a.dx && a.dx_acc && !make_map(&macc, a.dx_acc, a.T, a.d)))
+    return cudaErrorInvalidValue;
+  Params k{static_cast<const __nv_bfloat16*>(a.Wg),
+           a.mask,
+           reinterpret_cast<float*>(ws + p.dw),
+           reinterpret_cast<int32_t*>(ws + p.err),
+           a.T,
+           a.d,
+           a.E,
+           t.stride,
+           p.cols,
+           p.ranges,
+           p.tiles,
+           a.dx != nullptr,
+           a.dWg != nullptr,
+           a.dx && a.dx_acc};
+  auto go = [&](auto kern) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3(p.cols * p.ranges), dim3(kThreads), kSmem, s, 1, true, mx, mdz,
+                         macc, mdx, k);
+  };
+  if (t.blocks == 1) return go(route_products_tc_kernel<1>);
+  if (t.blocks == 2) return go(route_products_tc_kernel<2>);
+  return go(route_products_tc_kernel<3>);
+}
+
+}  // namespace moe
