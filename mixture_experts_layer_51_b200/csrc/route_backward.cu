@@ -73,12 +73,16 @@ __device__ __forceinline__ float bf16_round(float v) {
 
 // dz of 64 tokens, four threads a token (each a quarter of the experts, kept
 // in registers so that the scores are read once), and its column sums.  TC:
-// dz leaves as bf16 terms, else as fp32 rows of EP.
+// dz leaves as bf16 terms, else as fp32 rows of EP; either way by way of
+// shared memory, in whole 16-byte pieces of contiguous rows.
 template <bool TC>
 __global__ void __launch_bounds__(kDzThreads)
     route_dz_kernel(const RouteBackwardArgs a, int EP, DzTerms terms, void* __restrict__ dz,
                     float* __restrict__ bias_part, int32_t* __restrict__ err) {
+  // Rows start 16 bytes further round the banks than the one before.
+  constexpr int LD = 64 * 3 + 8;
   __shared__ float z[kRbTokens][kMaxE + 1];
+  __shared__ __align__(16) __nv_bfloat16 rows_s[TC ? kRbTokens * LD : 8];
   __shared__ float f[kMaxE];
   __shared__ float part[2][4][kRbTokens];
   const int tid = threadIdx.x, tok = tid % kRbTokens, q = tid / kRbTokens;
@@ -87,11 +91,6 @@ __global__ void __launch_bounds__(kDzThreads)
   pdl_trigger();
   if (blockIdx.x == 0 && tid == 0) *err = 0;
   const int n = a.counts ? *a.tokens : 0;
-  if (tid < kMaxE)
-    f[tid] = n > 0 && tid < a.E
-                 ? static_cast<float>(a.counts[tid]) / (static_cast<float>(n) * a.k)
-                 : 0.f;
-  const float c = n > 0 ? a.coef * (a.dloss ? *a.dloss : 1.f) * a.E / n : 0.f;
   const bool live = t < a.T && (!a.mask || a.mask[t]);
   const bool all = a.dgate && a.gating == MOE_GATE_SOFTMAX_TOPK;
   const bool loss = n > 0;
@@ -101,62 +100,83 @@ __global__ void __launch_bounds__(kDzThreads)
     const int e = q + 4 * i;
     p[i] = live && (loss || all) && e < a.E ? a.scores[static_cast<int64_t>(e) * a.T + t] : 0.f;
   }
-  const int64_t slot = static_cast<int64_t>(t) * a.k;
-  float total = 0.f, mean = 0.f;
-  if (live && a.dgate)
-    for (int j = q; j < a.k; j += 4) total = fmaf(a.gate[slot + j], a.dgate[slot + j], total);
-  __syncthreads();
+  // The token's slots q and q + 4.
+  int sel[2];
+  float g[2], dg[2];
 #pragma unroll
-  for (int i = 0; i < kMaxE / 4; ++i)
-    if (q + 4 * i < a.E) mean = fmaf(f[q + 4 * i], p[i], mean);
-  part[0][q][tok] = total;
+  for (int s = 0; s < 2; ++s) {
+    const int j = q + 4 * s;
+    const bool use = live && a.dgate && j < a.k;
+    const int64_t at = static_cast<int64_t>(t) * a.k + j;
+    sel[s] = use ? a.idx[at] : -1;
+    g[s] = use ? a.gate[at] : 0.f;
+    dg[s] = use ? a.dgate[at] : 0.f;
+  }
+  if (tid < kMaxE)
+    f[tid] = loss && tid < a.E
+                 ? static_cast<float>(a.counts[tid]) / (static_cast<float>(n) * a.k)
+                 : 0.f;
+  const float c = loss ? a.coef * (a.dloss ? *a.dloss : 1.f) * a.E / n : 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxE / 4; ++i) z[tok][q + 4 * i] = 0.f;
+  if (TC)  // the tail past the third term stays zero
+    for (int i = tid; i < kRbTokens * LD / 8; i += kDzThreads)
+      reinterpret_cast<uint4*>(rows_s)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  float mean = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxE / 4; ++i) mean = fmaf(f[q + 4 * i], p[i], mean);
+  part[0][q][tok] = fmaf(g[0], dg[0], g[1] * dg[1]);
   part[1][q][tok] = mean;
   __syncthreads();
-  total = (part[0][0][tok] + part[0][1][tok]) + (part[0][2][tok] + part[0][3][tok]);
+  const float total =
+      (part[0][0][tok] + part[0][1][tok]) + (part[0][2][tok] + part[0][3][tok]);
   mean = (part[1][0][tok] + part[1][1][tok]) + (part[1][2][tok] + part[1][3][tok]);
+  // The gates' terms at the selected experts, a quarter of the slots at a
+  // time: the same expert may come twice, so only one thread adds at once.
+  for (int turn = 0; turn < 4; ++turn) {
+    if (q == turn)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (sel[s] >= 0 && sel[s] < a.E)
+          z[tok][sel[s]] += all ? g[s] * dg[s] : g[s] * (dg[s] - total / a.gate_scale);
+    __syncthreads();
+  }
 #pragma unroll
   for (int i = 0; i < kMaxE / 4; ++i) {
     const int e = q + 4 * i;
-    float v = 0.f;
-    if (live && loss) v = c * p[i] * (f[e] - mean);
-    if (live && all) v -= p[i] * total;
+    if (e >= a.E) break;
+    float v = z[tok][e];
+    if (live && loss) v = fmaf(c * p[i], f[e] - mean, v);
+    if (live && all) v = fmaf(-p[i], total, v);
     z[tok][e] = v;
-  }
-  __syncthreads();
-  // One thread a token, slot after slot: the same expert may come twice.
-  if (q == 0 && live && a.dgate)
-    for (int j = 0; j < a.k; ++j) {
-      const int e = a.idx[slot + j];
-      if (e < 0 || e >= a.E) continue;
-      const float g = a.gate[slot + j], dg = a.dgate[slot + j];
-      z[tok][e] += all ? g * dg : g * (dg - total / a.gate_scale);
+    if (TC) {
+      const float hi = bf16_round(v), rest = isfinite(hi) ? v - hi : 0.f;
+      const float mid = bf16_round(rest);
+      __nv_bfloat16* row = rows_s + tok * LD + e;
+      row[0] = __float2bfloat16(hi);
+      row[terms.stride] = __float2bfloat16(mid);
+      row[2 * terms.stride] = __float2bfloat16(rest - mid);
     }
+  }
   __syncthreads();
   const int rows = min(kRbTokens, a.T - t0);
   if (TC) {
     const int chunks = 8 * terms.blocks;  // 16-byte chunks of a row
     uint4* out = static_cast<uint4*>(dz) + static_cast<int64_t>(t0) * chunks;
-    for (int i = tid; i < rows * chunks; i += kDzThreads) {
-      const int r = i / chunks, ch = i % chunks;
-      float v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int m = ch * 8 + u, term = m / terms.stride, e = m % terms.stride;
-        float w = term < 3 ? z[r][e] : 0.f;  // columns past E are zero
-        const float hi = bf16_round(w);
-        if (term > 0) w = isfinite(hi) ? w - hi : 0.f;
-        if (term > 1) w -= bf16_round(w);
-        v[u] = w;
-      }
-      out[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    }
+    const int ch = tid % 8;               // 8 x 32 threads: rows, then blocks
+    for (int r = tid / 8; r < rows; r += kDzThreads / 8)
+      for (int b = 0; b < terms.blocks; ++b)
+        out[r * chunks + b * 8 + ch] =
+            reinterpret_cast<const uint4*>(rows_s + r * LD)[b * 8 + ch];
   } else {
     float* out = static_cast<float*>(dz) + static_cast<int64_t>(t0) * EP;
-    for (int i = tid; i < rows * EP; i += kDzThreads) out[i] = z[i / EP][i % EP];
+    const int shift = __ffs(EP) - 1;      // EP is a power of two
+    for (int i = tid; i < rows * EP; i += kDzThreads) out[i] = z[i >> shift][i & (EP - 1)];
   }
   // tok is an expert here, q a quarter of the tokens.
   float s = 0.f;
+#pragma unroll
   for (int r = 0; r < kRbTokens / 4; ++r) s += z[q * (kRbTokens / 4) + r][tok];
   part[0][q][tok] = s;
   __syncthreads();

@@ -14,10 +14,12 @@
 // Bound by HBM: x is read once and dx written once; dz is re-read from L2 by
 // every column block.
 //
-// Warps: 0 TMA loads, 1 MMA issue, 2-3 zero the rows of padding tokens in x
-// (with a mask only: their x may hold anything, and 0 * NaN is NaN), 4-7
-// epilogue.  Every wait is bounded; a time-out raises the workspace's error
-// word and the CTA leaves after its copies and MMAs have landed.
+// Warps: 0 TMA loads, 1 MMA issue, 2 TMA stores (and the loads of dx_acc), 3
+// zeroes the rows of padding tokens in x (with a mask only: their x may hold
+// anything, and 0 * NaN is NaN), 4-11 epilogue, in two groups that take the
+// 64-column halves of the tiles in turn.  Every wait is bounded; a time-out
+// raises the workspace's error word and the CTA leaves after its copies and
+// MMAs have landed.
 
 #include <cudaTypedefs.h>
 
@@ -28,11 +30,17 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kEpilogue = 256;        // threads of warps 4-11
+constexpr int kThreads = 128 + kEpilogue;
 constexpr int kUnit = 128 * 64 * 2;   // 64 columns (or experts) of 128 rows: 16 KB
 constexpr int kMaxStages = 3;
 constexpr int kMaxUnits = 4;
 constexpr int kDwCol = 256;           // dW_g's first column in tensor memory
+// Tiles whose products the tensor cores sum up before the epilogue moves the
+// sum into fp32 registers.  The accumulators in tensor memory do not round
+// to nearest: over a whole range (16 tiles) dW_g came out 2.5e-6 off, twice
+// to ten times what sums that round are off.
+constexpr int kFlush = 4;
 constexpr int kSmem = 14 * kUnit + 2048;  // + control block and alignment
 
 // NB: 64-element blocks of a dz row.  Stages x (2 + NB), W_g blocks and
@@ -52,10 +60,10 @@ static_assert(Cfg<1>::CTL_OFF == 14 * kUnit && Cfg<2>::CTL_OFF == 14 * kUnit &&
               Cfg<3>::CTL_OFF == 14 * kUnit, "one shared-memory size");
 
 struct Ctl {
-  uint64_t full[kMaxStages], empty[kMaxStages], ready[kMaxStages];
-  uint64_t tfull[2], tempty[2];
-  uint64_t accfull[kMaxUnits];
-  uint64_t wready, drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
+  uint64_t tfull[2], tempty[2];                    // dx accumulators
+  uint64_t uready[kMaxUnits], ustaged[kMaxUnits];  // staging units
+  uint64_t dwfull, dwempty, wready, drain;
   uint32_t tmem_base;
   volatile int abort_flag;
 };
@@ -79,17 +87,19 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
   return static_cast<uint32_t>(r * 128 + ((ch ^ (r & 7)) << 4));
 }
 
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// The same, and whether all 128 threads say so: one answer for all of them.
+__device__ __forceinline__ void epilogue_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory");
+}
+// The same, and whether all threads say so: one answer for all of them.
 __device__ __forceinline__ bool epilogue_all(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred p, 1, 128, q;\n\t"
+      "bar.red.and.pred p, 1, %2, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(all)
-      : "r"(static_cast<uint32_t>(ok))
+      : "r"(static_cast<uint32_t>(ok)), "n"(kEpilogue)
       : "memory");
   return all != 0;
 }
@@ -113,19 +123,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ntiles =
       static_cast<int>(static_cast<int64_t>(range + 1) * p.tiles / p.ranges) - tile0;
   const int halves = c0 + 64 < p.d ? 2 : 1;  // 64-column halves that exist
+  const int units = p.want_dx ? ntiles * halves : 0;
 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(smem_u32(&c.full[i]), 1);
       mbar_init(smem_u32(&c.empty[i]), 1);
-      mbar_init(smem_u32(&c.ready[i]), 64);
+      mbar_init(smem_u32(&c.clean[i]), 32);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&c.tfull[i]), 1);
-      mbar_init(smem_u32(&c.tempty[i]), 4);
+      mbar_init(smem_u32(&c.tempty[i]), 4 * halves);
     }
-    for (int i = 0; i < C::UNITS; ++i) mbar_init(smem_u32(&c.accfull[i]), 1);
-    mbar_init(smem_u32(&c.wready), kThreads - 64);
+    for (int i = 0; i < C::UNITS; ++i) {
+      mbar_init(smem_u32(&c.uready[i]), 1);
+      mbar_init(smem_u32(&c.ustaged[i]), 128);
+    }
+    mbar_init(smem_u32(&c.dwfull), 1);
+    mbar_init(smem_u32(&c.dwempty), kEpilogue / 32);
+    mbar_init(smem_u32(&c.wready), kEpilogue);
     mbar_init(smem_u32(&c.drain), 1);
     c.abort_flag = 0;
     fence_mbar_init();
@@ -134,6 +150,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tmem_alloc(smem_u32(&c.tmem_base), 512);
     tmem_relinquish();
+  }
+  if (tid == 64) {
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmDz);
+    tma_prefetch_desc(&tmAcc);
+    tma_prefetch_desc(&tmDx);
   }
   tc_fence_before();
   __syncthreads();
@@ -176,12 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t wdesc = smem_desc_sw128(base + C::W_OFF, 16, 1024);
       bool ok = mbar_wait(smem_u32(&c.wready), 0);
       if (!ok) give_up(p, c, kErrTimeoutMma);
-      int stage = 0;
+      int stage = 0, flushed = 0;
       uint32_t phase = 0;
       for (int i = 0; ok && i < ntiles; ++i) {
         const int buf = i & 1;
         ok = !c.abort_flag &&
-             mbar_wait(smem_u32(p.mask ? &c.ready[stage] : &c.full[stage]), phase) &&
+             mbar_wait(smem_u32(p.mask ? &c.clean[stage] : &c.full[stage]), phase) &&
              (!p.want_dx || mbar_wait(smem_u32(&c.tempty[buf]), ((i >> 1) & 1) ^ 1));
         if (!ok) {
           give_up(p, c, kErrTimeoutMma);
@@ -203,6 +225,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit(smem_u32(&c.tfull[buf]));
         }
         if (p.want_dw) {
+          const bool first = i % kFlush == 0;
+          if (first && i > 0 && !mbar_wait(smem_u32(&c.dwempty), (flushed++) & 1)) {
+            give_up(p, c, kErrTimeoutMma);
+            break;
+          }
+          tc_fence_after();
           // 16 tokens are 16 rows of 128 bytes; 64-wide blocks lie 16 KB apart.
           const uint64_t adesc = smem_desc_sw128(src, kUnit, 1024);
           const uint64_t bdesc = smem_desc_sw128(src + 2 * kUnit, kUnit, 1024);
@@ -210,152 +238,190 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < kRbTcTokens / 16; ++kk)
             tc_mma_bf16(tmem + kDwCol, adesc + static_cast<uint64_t>((kk * 2048) >> 4),
                         bdesc + static_cast<uint64_t>((kk * 2048) >> 4), idesc_dw,
-                        (i > 0 || kk > 0) ? 1u : 0u);
+                        (!first || kk > 0) ? 1u : 0u);
+          if (i % kFlush == kFlush - 1 || i == ntiles - 1) tc_commit(smem_u32(&c.dwfull));
         }
         tc_commit(smem_u32(&c.empty[stage]));
         if (++stage == C::STAGES) stage = 0, phase ^= 1;
       }
+      // Every MMA has completed before tensor memory is freed.
       tc_commit(smem_u32(&c.drain));
       if (!mbar_wait(smem_u32(&c.drain), 0)) give_up(p, c, kErrTimeoutDrain);
     }
-  } else {
-    // W_g of the block as the K-major operand, term after term, zero past the
-    // last expert and column.
-    for (int i = tid - 64; i < C::WB * 128 * 64; i += kThreads - 64) {
-      const int b = i / (128 * 64), r = i / 64 % 128, j = i % 64;
-      const int n = 64 * b + j, e = NB == 3 ? n : n % p.stride;
-      const bool in = c0 + r < p.d && e < p.E && n < (NB == 3 ? p.E : 3 * p.stride);
-      const __nv_bfloat16 w = in && p.want_dx ? p.Wg[static_cast<int64_t>(c0 + r) * p.E + e]
-                                              : __float2bfloat16(0.f);
-      *reinterpret_cast<__nv_bfloat16*>(smem + C::W_OFF + b * kUnit + swz(r, j / 8) + j % 8 * 2) = w;
-    }
-    fence_async_shared();
-    mbar_arrive(smem_u32(&c.wready));
-    if (warp < 4) {
-      // ------------------------------------------- rows of padding tokens
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int i = 0; p.mask && i < ntiles; ++i) {
-        if (c.abort_flag || !mbar_wait(smem_u32(&c.full[stage]), phase)) {
-          give_up(p, c, kErrTimeoutMma);
+  } else if (warp == 2) {
+    if (lane == 0) {
+      // ---------------------------------------- staging units and stores
+      // A unit is ready when its last store has left and, with dx_acc, the
+      // tile's part of that has arrived.
+      auto make_ready = [&](int u) {
+        const uint32_t bar = smem_u32(&c.uready[u % C::UNITS]);
+        if (!p.add) {
+          mbar_arrive(bar);
+          return;
+        }
+        mbar_arrive_expect_tx(bar, kUnit);
+        tma_load_2d(base + C::OUT_OFF + (u % C::UNITS) * kUnit, &tmAcc, bar,
+                    c0 + 64 * (u % halves), (tile0 + u / halves) * kRbTcTokens);
+      };
+      int readied = 0;
+      for (; readied < C::UNITS && readied < units; ++readied) make_ready(readied);
+      for (int u = 0; u < units; ++u) {
+        const int slot = u % C::UNITS;
+        if (c.abort_flag || !mbar_wait(smem_u32(&c.ustaged[slot]), (u / C::UNITS) & 1)) {
+          give_up(p, c, kErrTimeoutEpilogue);
           break;
         }
-        for (int r = tid - 64; r < kRbTcTokens; r += 64) {
-          const int t = (tile0 + i) * kRbTcTokens + r;
-          if (!p.want_dw || t >= p.T || p.mask[t]) continue;
-          for (int h = 0; h < halves; ++h)
+        tma_store_2d(&tmDx, base + C::OUT_OFF + slot * kUnit, c0 + 64 * (u % halves),
+                     (tile0 + u / halves) * kRbTcTokens);
+        bulk_commit();
+        if (readied < units) {
+          bulk_wait_read<0>();
+          make_ready(readied++);
+        }
+      }
+      bulk_wait<0>();
+      // No load of dx_acc may land after the CTA has left.
+      for (int u = readied > C::UNITS ? readied - C::UNITS : 0; u < readied; ++u)
+        if (!mbar_wait(smem_u32(&c.uready[u % C::UNITS]), (u / C::UNITS) & 1))
+          give_up(p, c, kErrTimeoutDrain);
+    }
+  } else if (warp == 3) {
+    // --------------------------------------------- rows of padding tokens
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; p.mask && i < ntiles; ++i) {
+      if (c.abort_flag || !mbar_wait(smem_u32(&c.full[stage]), phase)) {
+        give_up(p, c, kErrTimeoutMma);
+        break;
+      }
+      for (int r = lane; p.want_dw && r < kRbTcTokens; r += 32) {
+        const int t = (tile0 + i) * kRbTcTokens + r;
+        if (t >= p.T || p.mask[t]) continue;
+        for (int h = 0; h < halves; ++h)
 #pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-              *reinterpret_cast<uint4*>(smem + stage * C::STAGE + h * kUnit + r * 128 + ch * 16) =
-                  make_uint4(0, 0, 0, 0);
+          for (int ch = 0; ch < 8; ++ch)
+            *reinterpret_cast<uint4*>(smem + stage * C::STAGE + h * kUnit + r * 128 + ch * 16) =
+                make_uint4(0, 0, 0, 0);
+      }
+      fence_async_shared();
+      mbar_arrive(smem_u32(&c.clean[stage]));
+      if (++stage == C::STAGES) stage = 0, phase ^= 1;
+    }
+  } else {
+    // --------------------------------------------------------- epilogue
+    const int et = tid - 128, group = et >> 7, q = warp & 3, row = q * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    {
+      // W_g of the block as the K-major operand: term after term, zero past
+      // the last expert and column.  Thread (row, group) makes half of a row.
+      const int col = c0 + row;
+      const __nv_bfloat16* w = p.Wg + static_cast<int64_t>(col) * p.E;
+      const bool in = p.want_dx && col < p.d;
+      constexpr int HALF = 32 * C::WB;
+      int e = NB == 3 ? group * HALF : group * HALF % p.stride;
+      int left = (NB == 3 ? p.E : 3 * p.stride) - group * HALF;  // elements that are not zero
+#pragma unroll
+      for (int ch = 0; ch < HALF / 8; ++ch) {
+        uint32_t v[4];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t b =
+              in && left > 0 ? static_cast<uint32_t>(__bfloat16_as_ushort(w[e])) : 0u;
+          v[u / 2] = u % 2 ? v[u / 2] | (b << 16) : b;
+          --left;
+          if (++e == p.stride) e = 0;
+        }
+        const int n = group * HALF / 8 + ch;  // 16-byte chunk of the row
+        *reinterpret_cast<uint4*>(smem + C::W_OFF + n / 8 * kUnit + swz(row, n % 8)) =
+            make_uint4(v[0], v[1], v[2], v[3]);
+      }
+      fence_async_shared();
+      mbar_arrive(smem_u32(&c.wready));
+    }
+    // dW_g so far: lane = column; 32 NB of the block's columns a thread, the
+    // three terms of one expert already added where their places are known.
+    constexpr int ACC = NB == 3 ? 32 : 32 * NB;
+    float acc[ACC];
+#pragma unroll
+    for (int e = 0; e < ACC; ++e) acc[e] = 0.f;
+    int u = group, flushes = 0;
+    bool ok = true;
+    for (int i = 0; i < ntiles && ok; ++i) {
+      for (; ok && u < units && u / halves == i; u += 2) {
+        const int buf = i & 1, slot = u % C::UNITS;
+        ok = __all_sync(0xffffffffu,
+                        !c.abort_flag && mbar_wait(smem_u32(&c.tfull[buf]), (i >> 1) & 1) &&
+                            mbar_wait(smem_u32(&c.uready[slot]), (u / C::UNITS) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        float v[2][32];
+        const uint32_t src = tmem + lane_base + buf * 128 + u % halves * 64;
+        tc_ld_32cols(src, v[0]);
+        tc_ld_32cols(src + 32, v[1]);
+        tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.tempty[buf]));
+        uint8_t* out = smem + C::OUT_OFF + slot * kUnit;
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          uint4* at = reinterpret_cast<uint4*>(out + swz(row, ch));
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = v[ch / 4][ch % 4 * 8 + e];
+          if (p.add) {
+            const uint4 a = *at;
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[2 * e] += __uint_as_float(w[e] << 16);
+              f[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+            }
+          }
+          *at = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                           pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
         }
         fence_async_shared();
-        mbar_arrive(smem_u32(&c.ready[stage]));
-        if (++stage == C::STAGES) stage = 0, phase ^= 1;
+        mbar_arrive(smem_u32(&c.ustaged[slot]));
       }
-    } else {
-      // ------------------------------------------------------- epilogue
-      const int q = warp - 4, row = q * 32 + lane;
-      const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-      const bool leader = tid == 128;
-      if (p.want_dx) {
-        const int units = ntiles * halves;
-        auto load_acc = [&](int u) {  // dx_acc of unit u into its staging block
-          const uint32_t bar = smem_u32(&c.accfull[u % C::UNITS]);
-          mbar_arrive_expect_tx(bar, kUnit);
-          tma_load_2d(base + C::OUT_OFF + (u % C::UNITS) * kUnit, &tmAcc, bar,
-                      c0 + 64 * (u % halves), (tile0 + u / halves) * kRbTcTokens);
-        };
-        int loaded = 0;
-        if (p.add && leader)
-          for (; loaded < C::UNITS && loaded < units; ++loaded) load_acc(loaded);
-        int done = 0;
-        for (int u = 0; u < units; ++u) {
-          const int i = u / halves, h = u % halves, buf = i & 1, slot = u % C::UNITS;
-          bool ok = !c.abort_flag;
-          if (ok && h == 0) ok = mbar_wait(smem_u32(&c.tfull[buf]), (i >> 1) & 1);
-          if (ok && p.add) ok = mbar_wait(smem_u32(&c.accfull[slot]), (u / C::UNITS) & 1);
-          if (!ok) give_up(p, c, kErrTimeoutEpilogue);
-          if (!epilogue_all(ok)) break;
-          tc_fence_after();
-          float v[2][32];
-          const uint32_t src = tmem + lane_base + buf * 128 + h * 64;
-          tc_ld_32cols(src, v[0]);
-          tc_ld_32cols(src + 32, v[1]);
+      if (ok && p.want_dw && (i % kFlush == kFlush - 1 || i == ntiles - 1)) {
+        ok = __all_sync(0xffffffffu,
+                        !c.abort_flag && mbar_wait(smem_u32(&c.dwfull), (flushes++) & 1));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float v[32];
+          tc_ld_32cols(tmem + lane_base + kDwCol +
+                           (NB == 3 ? (2 - b) * 64 + group * 32 : (group * NB + b) * 32), v);
           tc_wait_ld();
-          if (h == halves - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c.tempty[buf]));
-          }
-          uint8_t* out = smem + C::OUT_OFF + slot * kUnit;
 #pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            uint4* at = reinterpret_cast<uint4*>(out + swz(row, ch));
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = v[ch / 4][ch % 4 * 8 + e];
-            if (p.add) {
-              const uint4 a = *at;
-              const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                f[2 * e] += __uint_as_float(w[e] << 16);
-                f[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
-              }
-            }
-            uint4 o;
-            o.x = pack_bf16x2(f[0], f[1]);
-            o.y = pack_bf16x2(f[2], f[3]);
-            o.z = pack_bf16x2(f[4], f[5]);
-            o.w = pack_bf16x2(f[6], f[7]);
-            *at = o;
-          }
-          fence_async_shared();
-          epilogue_sync();
-          ++done;
-          if (leader) {
-            tma_store_2d(&tmDx, base + C::OUT_OFF + slot * kUnit, c0 + 64 * h,
-                         (tile0 + i) * kRbTcTokens);
-            bulk_commit();
-            // Unit u - 1 has left its block: its place is free for unit
-            // u - 1 + UNITS, and, with three blocks or more, the block of
-            // unit u + 2 is free before any thread gets there.
-            bulk_wait_read<1>();
-            if (p.add && u >= 1 && loaded < units) load_acc(loaded++);
-          }
+          for (int e = 0; e < 32; ++e) acc[(NB == 3 ? 0 : b * 32) + e] += v[e];
         }
-        if (leader) {
-          bulk_wait<0>();
-          // Loads that no iteration waited for (only after a time-out).
-          for (int u = done; u < loaded; ++u)
-            mbar_wait(smem_u32(&c.accfull[u % C::UNITS]), (u / C::UNITS) & 1);
-        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.dwempty));
       }
-      if (p.want_dw) {
-        // dW_g: lane = column.  The terms of one expert lie `stride` apart, so
-        // they are added through shared memory (the ring is idle by now).
-        bool ok = !c.abort_flag && mbar_wait(smem_u32(&c.drain), 0);
-        if (!ok) give_up(p, c, kErrTimeoutEpilogue);
-        if (epilogue_all(ok)) {
-          tc_fence_after();
-          float* rows = reinterpret_cast<float*>(smem);
-          constexpr int LD = 64 * NB + 1;
-          for (int b = 0; b < 2 * NB; ++b) {
-            float v[32];
-            tc_ld_32cols(tmem + lane_base + kDwCol + b * 32, v);
-            tc_wait_ld();
+    }
+    if (!ok) give_up(p, c, kErrTimeoutEpilogue);
+    if (p.want_dw && epilogue_all(ok)) {
+      // The last flush came after the last MMA: the ring is idle, and the
+      // rows go through it so that they leave in whole lines.
+      float* rows = reinterpret_cast<float*>(smem);
+      constexpr int LD = 2 * ACC + 1;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) rows[row * LD + b * 32 + e] = v[e];
-          }
-          epilogue_sync();
-          const int n = min(kRbTcCols, p.d - c0) * p.E;
-          float* out = p.dw + (static_cast<int64_t>(range) * p.d + c0) * p.E;
-          for (int i = tid - 128; i < n; i += 128) {
-            const float* r = rows + (i / p.E) * LD + i % p.E;
-            out[i] = r[2 * p.stride] + r[p.stride] + r[0];
-          }
-        }
+      for (int e = 0; e < ACC; ++e) rows[row * LD + group * ACC + e] = acc[e];
+      epilogue_sync();
+      const int n = min(kRbTcCols, p.d - c0) * p.E;
+      float* out = p.dw + (static_cast<int64_t>(range) * p.d + c0) * p.E;
+      int r = et / p.E, e = et % p.E;
+      const int dr = kEpilogue / p.E, de = kEpilogue % p.E;
+      for (int i = et; i < n; i += kEpilogue) {
+        const float* at = rows + r * LD + e;
+        out[i] = NB == 3 ? at[0] : at[2 * p.stride] + at[p.stride] + at[0];
+        r += dr;
+        e += de;
+        if (e >= p.E) e -= p.E, ++r;
       }
     }
   }
