@@ -9,13 +9,14 @@
 //   balance loss:        dz_e += dL coef (E / N) p_e (f_e - sum_i f_i p_i)
 //   dx = dx_acc + dz W_g^T,   dW_g = x^T dz,   dbias = sum_t dz
 //
-// Three launches.  (1) dz for every token, and its column sums per block of
+// Two launches.  (1) dz for every token, and its column sums per block of
 // tokens.  (2) Both products in one pass over x: a CTA owns a block of
 // columns and a range of tokens, so each x element is read once, each dx
 // element written once, and dW_g of the block stays on the chip until the
 // range is done (bf16: tensor cores, route_backward_tc.cu; fp32: FMA, here).
-// (3) The ranges' dW_g and the blocks' column sums added in order (no
-// floating-point atomics).
+// The last range of a column block to finish adds all of the block's ranges
+// in order, and one warp an expert the dz blocks' column sums, so no sum
+// depends on scheduling (no floating-point atomics).
 
 #include "route_backward.cuh"
 
@@ -29,7 +30,7 @@ constexpr int kThreads = 256;
 
 // Token ranges for `cols` column blocks: the number that needs the fewest
 // tile times, where a wave of kRbSms CTAs takes the tiles of its longest
-// range and about two more for its start and its end.
+// range and about five more for its start and its end.
 int pick_ranges(int cols, int tiles, int per_sm) {
   int best = 1;
   int64_t best_cost = INT64_MAX;
@@ -37,7 +38,7 @@ int pick_ranges(int cols, int tiles, int per_sm) {
   const int most = tiles < 2 * slots / cols + 1 ? tiles : 2 * slots / cols + 1;
   for (int r = 1; r <= most; ++r) {
     const int64_t waves = (static_cast<int64_t>(cols) * r + slots - 1) / slots;
-    const int64_t cost = waves * ((tiles + r - 1) / r + 2);
+    const int64_t cost = waves * ((tiles + r - 1) / r + 5);
     if (cost < best_cost) best_cost = cost, best = r;
   }
   return best;
@@ -59,6 +60,7 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
     return here;
   };
   p.err = take(sizeof(int32_t));
+  p.tickets = take(sizeof(uint32_t) * p.cols);
   const size_t row = tc ? 128 * dz_terms(E).blocks : sizeof(float) * p.EP;
   p.dz = take(row * T);
   p.bias = take(sizeof(float) * kMaxE * p.blocks);
@@ -78,7 +80,8 @@ __device__ __forceinline__ float bf16_round(float v) {
 template <bool TC>
 __global__ void __launch_bounds__(kDzThreads)
     route_dz_kernel(const RouteBackwardArgs a, int EP, DzTerms terms, void* __restrict__ dz,
-                    float* __restrict__ bias_part, int32_t* __restrict__ err) {
+                    float* __restrict__ bias_part, int32_t* __restrict__ err,
+                    uint32_t* __restrict__ tickets, int ntickets) {
   // Rows start 16 bytes further round the banks than the one before.
   constexpr int LD = 64 * 3 + 8;
   __shared__ float z[kRbTokens][kMaxE + 1];
@@ -89,16 +92,23 @@ __global__ void __launch_bounds__(kDzThreads)
   const int t0 = blockIdx.x * kRbTokens, t = t0 + tok;
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && tid == 0) *err = 0;
-  const int n = a.counts ? *a.tokens : 0;
-  const bool live = t < a.T && (!a.mask || a.mask[t]);
+  if (blockIdx.x == 0) {
+    if (tid == 0) *err = 0;
+    for (int i = tid; i < ntickets; i += kDzThreads) tickets[i] = 0;
+  }
+  // Every load before the first use of any (a padding token's values are
+  // loaded and dropped, which is quicker than to wait for its mask).
+  const bool in = t < a.T;
   const bool all = a.dgate && a.gating == MOE_GATE_SOFTMAX_TOPK;
-  const bool loss = n > 0;
+  const int n = a.counts ? *a.tokens : 0;
+  const float dloss = a.counts && a.dloss ? *a.dloss : 1.f;
+  const int count = a.counts && tid < a.E ? a.counts[tid] : 0;
+  const bool live = in && (!a.mask || a.mask[t]);
   float p[kMaxE / 4];
 #pragma unroll
   for (int i = 0; i < kMaxE / 4; ++i) {
     const int e = q + 4 * i;
-    p[i] = live && (loss || all) && e < a.E ? a.scores[static_cast<int64_t>(e) * a.T + t] : 0.f;
+    p[i] = in && (a.counts || all) && e < a.E ? a.scores[static_cast<int64_t>(e) * a.T + t] : 0.f;
   }
   // The token's slots q and q + 4.
   int sel[2];
@@ -106,19 +116,24 @@ __global__ void __launch_bounds__(kDzThreads)
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int j = q + 4 * s;
-    const bool use = live && a.dgate && j < a.k;
+    const bool use = in && a.dgate && j < a.k;
     const int64_t at = static_cast<int64_t>(t) * a.k + j;
     sel[s] = use ? a.idx[at] : -1;
     g[s] = use ? a.gate[at] : 0.f;
     dg[s] = use ? a.dgate[at] : 0.f;
   }
+  const bool loss = n > 0;
   if (tid < kMaxE)
-    f[tid] = loss && tid < a.E
-                 ? static_cast<float>(a.counts[tid]) / (static_cast<float>(n) * a.k)
-                 : 0.f;
-  const float c = loss ? a.coef * (a.dloss ? *a.dloss : 1.f) * a.E / n : 0.f;
+    f[tid] = loss ? static_cast<float>(count) / (static_cast<float>(n) * a.k) : 0.f;
+  const float c = loss ? a.coef * dloss * a.E / n : 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxE / 4; ++i) z[tok][q + 4 * i] = 0.f;
+  for (int i = 0; i < kMaxE / 4; ++i) {
+    z[tok][q + 4 * i] = 0.f;
+    if (!live) p[i] = 0.f;
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (!live) sel[s] = -1, g[s] = dg[s] = 0.f;
   if (TC)  // the tail past the third term stays zero
     for (int i = tid; i < kRbTokens * LD / 8; i += kDzThreads)
       reinterpret_cast<uint4*>(rows_s)[i] = make_uint4(0, 0, 0, 0);
@@ -190,8 +205,8 @@ __global__ void __launch_bounds__(kDzThreads)
 // in registers, and makes dx for a quarter of the tile's tokens.
 template <int EP>
 __global__ void __launch_bounds__(kThreads)
-    route_products_kernel(const RouteBackwardArgs a, int ranges, int tiles,
-                          const float* __restrict__ dz, float* __restrict__ dw) {
+    route_products_kernel(const RouteBackwardArgs a, const RouteSums sums, int ranges, int tiles,
+                          const float* __restrict__ dz) {
   constexpr int QE = EP / 4;
   __shared__ __align__(16) float dz_s[kTile][EP];
   __shared__ float x_s[kTile][kCols];
@@ -240,56 +255,39 @@ __global__ void __launch_bounds__(kThreads)
         dx[at] = dx_acc ? v + dx_acc[at] : v;
       }
   }
-  if (a.dWg && in)
+  if (sums.dbias && tid < 32)
+    for (int e = blockIdx.x + blockIdx.y * gridDim.x; e < a.E; e += gridDim.x * gridDim.y)
+      sum_bias(sums, e, tid);
+  if (!a.dWg) return;
+  if (in)
 #pragma unroll
     for (int e = 0; e < QE; ++e)
       if (q * QE + e < a.E)
-        dw[(static_cast<int64_t>(blockIdx.y) * a.d + c) * a.E + q * QE + e] = acc[e];
+        sums.dw[(static_cast<int64_t>(blockIdx.y) * a.d + c) * a.E + q * QE + e] = acc[e];
+  __shared__ uint32_t last;
+  __threadfence();
+  __syncthreads();
+  if (tid == 0)
+    last = atomicAdd(sums.tickets + blockIdx.x, 1u) + 1 == static_cast<uint32_t>(ranges);
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  sum_ranges(sums, blockIdx.x * kCols, min(kCols, a.d - static_cast<int>(blockIdx.x) * kCols), tid,
+             kThreads);
 }
 
-// The ranges' dW_g (CTAs 0 .. dw_ctas - 1, four elements a thread) and the
-// blocks' column sums (one CTA an expert), each in a fixed order.  After a
-// time-out in the products nothing here is right: NaN says so.
-__global__ void __launch_bounds__(kThreads)
-    route_finish_kernel(const float* __restrict__ dw, const float* __restrict__ bias_part,
-                        const int32_t* __restrict__ err, int ranges, int blocks, int64_t n,
-                        int dw_ctas, float* __restrict__ dWg, float* __restrict__ dbias) {
-  __shared__ float warp_sum[kThreads / 32];
-  const int tid = threadIdx.x;
+// The bias alone: one warp an expert.
+__global__ void __launch_bounds__(32) route_bias_kernel(const RouteSums sums) {
   pdl_wait();
   pdl_trigger();
-  const bool failed = ranges > 0 && *err != 0;
-  if (static_cast<int>(blockIdx.x) < dw_ctas) {
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + tid) * 4;
-    if (i >= n) return;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int r = 0; r < ranges; ++r) {
-      const float4 v = *reinterpret_cast<const float4*>(dw + r * n + i);
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
-    if (failed) s.x = s.y = s.z = s.w = __int_as_float(0x7fc00000);
-    *reinterpret_cast<float4*>(dWg + i) = s;
-    return;
-  }
-  const int e = blockIdx.x - dw_ctas;
-  float s = 0.f;
-  for (int b = tid; b < blocks; b += kThreads) s += bias_part[static_cast<int64_t>(b) * kMaxE + e];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (tid % 32 == 0) warp_sum[tid / 32] = s;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) s += warp_sum[w];
-    dbias[e] = s;
-  }
+  sum_bias(sums, blockIdx.x, threadIdx.x);
 }
 
 cudaError_t launch_products(const RouteBackwardArgs& a, const RouteBackwardPlan& p,
-                            const float* dz, float* dw, cudaStream_t s) {
+                            const RouteSums& sums, const float* dz, cudaStream_t s) {
   auto go = [&](auto kern) {
-    return launch_kernel(kern, dim3(p.cols, p.ranges), dim3(kThreads), 0, s, 1, true, a, p.ranges,
-                         p.tiles, dz, dw);
+    return launch_kernel(kern, dim3(p.cols, p.ranges), dim3(kThreads), 0, s, 1, true, a, sums,
+                         p.ranges, p.tiles, dz);
   };
   switch (p.EP) {
     case 8: return go(route_products_kernel<8>);
@@ -306,31 +304,36 @@ size_t route_backward_scratch_bytes(int T, int d, int E, moe_dtype dtype) {
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, moe_dtype dtype, cudaStream_t s) {
+  if (a.T == 0) {
+    cudaError_t err = cudaSuccess;
+    if (a.dWg) err = cudaMemsetAsync(a.dWg, 0, sizeof(float) * a.d * a.E, s);
+    if (a.dbias && err == cudaSuccess) err = cudaMemsetAsync(a.dbias, 0, sizeof(float) * a.E, s);
+    return err;
+  }
   const RouteBackwardPlan p = make_plan(a.T, a.d, a.E, dtype);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  int32_t* err_word = reinterpret_cast<int32_t*>(ws + p.err);
-  float* bias_part = reinterpret_cast<float*>(ws + p.bias);
-  float* dw = reinterpret_cast<float*>(ws + p.dw);
-  cudaError_t err = cudaSuccess;
-  if (a.T > 0) {
-    auto dz = [&](auto kern) {
-      return launch_kernel(kern, dim3(p.blocks), dim3(kDzThreads), 0, s, 1, true, a, p.EP,
-                           dz_terms(a.E), static_cast<void*>(ws + p.dz), bias_part, err_word);
-    };
-    const bool tc = dtype == MOE_BF16;
-    err = tc ? dz(route_dz_kernel<true>) : dz(route_dz_kernel<false>);
-    if (err == cudaSuccess && (a.dx || a.dWg))
-      err = tc ? launch_route_products_tc(a, p, s)
-               : launch_products(a, p, reinterpret_cast<const float*>(ws + p.dz), dw, s);
-    if (err != cudaSuccess) return err;
-  }
-  if (!a.dWg && !a.dbias) return cudaSuccess;
-  const int64_t n = static_cast<int64_t>(a.d) * a.E;
-  const int dw_ctas = a.dWg ? static_cast<int>((n / 4 + kThreads - 1) / kThreads) : 0;
-  return launch_kernel(route_finish_kernel, dim3(dw_ctas + (a.dbias ? a.E : 0)), dim3(kThreads), 0,
-                       s, 1, true, static_cast<const float*>(dw),
-                       static_cast<const float*>(bias_part), static_cast<const int32_t*>(err_word),
-                       p.ranges, p.blocks, n, dw_ctas, a.dWg, a.dbias);
+  float* bias = reinterpret_cast<float*>(ws + p.bias);
+  const RouteSums sums{bias,
+                       reinterpret_cast<float*>(ws + p.dw),
+                       reinterpret_cast<int32_t*>(ws + p.err),
+                       reinterpret_cast<uint32_t*>(ws + p.tickets),
+                       a.dWg,
+                       a.dbias,
+                       p.blocks,
+                       p.ranges,
+                       a.d,
+                       a.E};
+  const bool tc = dtype == MOE_BF16;
+  auto dz = [&](auto kern) {
+    return launch_kernel(kern, dim3(p.blocks), dim3(kDzThreads), 0, s, 1, true, a, p.EP,
+                         dz_terms(a.E), static_cast<void*>(ws + p.dz), bias, sums.err,
+                         sums.tickets, p.cols);
+  };
+  const cudaError_t err = tc ? dz(route_dz_kernel<true>) : dz(route_dz_kernel<false>);
+  if (err != cudaSuccess) return err;
+  if (!a.dx && !a.dWg) return launch_kernel(route_bias_kernel, dim3(a.E), dim3(32), 0, s, 1, true, sums);
+  return tc ? launch_route_products_tc(a, p, sums, s)
+            : launch_products(a, p, sums, reinterpret_cast<const float*>(ws + p.dz), s);
 }
 
 }  // namespace moe

@@ -29,11 +29,70 @@ struct RouteBackwardPlan {
   int cols;    // column blocks of the products
   int ranges;  // token ranges of the products
   int tiles;   // token tiles, shared out over the ranges
-  size_t err, dz, bias, dw, total;  // byte offsets
+  size_t err, tickets, dz, bias, dw, total;  // byte offsets
 };
 
+// What the products kernels share to finish in the same launch.  `tickets`
+// (one a column block, zeroed by the dz kernel of the same call) tells the
+// last of a block's ranges to finish, whichever that is, to add them all up
+// in order; `bias` are the dz blocks' column sums [blocks][kMaxE].
+struct RouteSums {
+  const float* bias;
+  float* dw;          // [ranges, d, E]
+  int32_t* err;
+  uint32_t* tickets;
+  float* dWg;         // null: not wanted
+  float* dbias;
+  int blocks, ranges, d, E;
+};
+
+// dbias of expert e by one warp: lanes over the blocks, then a tree.
+__device__ __forceinline__ void sum_bias(const RouteSums& s, int e, int lane) {
+  float v = 0.f;
+#pragma unroll 4
+  for (int b = lane; b < s.blocks; b += 32) v += s.bias[static_cast<int64_t>(b) * kMaxE + e];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0) s.dbias[e] = v;
+}
+
+// dW_g of columns c0 .. c0 + cols - 1: the ranges' parts in order, by `n`
+// threads (this one is `i`).  After a time-out in the products nothing here
+// is right: NaN says so.
+__device__ __forceinline__ void sum_ranges(const RouteSums& s, int c0, int cols, int i, int n) {
+  const int64_t plane = static_cast<int64_t>(s.d) * s.E;
+  const int64_t at = static_cast<int64_t>(c0) * s.E;
+  const bool failed = *static_cast<volatile int32_t*>(s.err) != 0;
+  const int count = cols * s.E / 4;  // columns come in eights
+  const float4* from = reinterpret_cast<const float4*>(s.dw + at);
+  float4* to = reinterpret_cast<float4*>(s.dWg + at);
+  // Eight pieces at a time: one thread block reads what a whole column block
+  // wrote, so what counts is how many loads are on their way.
+  constexpr int P = 8;
+  for (int v0 = i; v0 < count; v0 += P * n) {
+    float4 sum[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int r = 0; r < s.ranges; ++r) {
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        if (v0 + j * n >= count) continue;
+        const float4 part = __ldcg(from + r * (plane / 4) + v0 + j * n);
+        sum[j].x += part.x, sum[j].y += part.y, sum[j].z += part.z, sum[j].w += part.w;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      if (v0 + j * n >= count) continue;
+      if (failed) sum[j].x = sum[j].y = sum[j].z = sum[j].w = __int_as_float(0x7fc00000);
+      to[v0 + j * n] = sum[j];
+    }
+  }
+}
+
 cudaError_t launch_route_products_tc(const RouteBackwardArgs& a, const RouteBackwardPlan& p,
-                                     cudaStream_t s);
+                                     const RouteSums& sums, cudaStream_t s);
 constexpr int kRbTcCols = 128;   // columns and tokens of one tile
 constexpr int kRbTcTokens = 128;
 

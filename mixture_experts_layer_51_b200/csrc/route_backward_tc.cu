@@ -65,20 +65,20 @@ struct Ctl {
   uint64_t uready[kMaxUnits], ustaged[kMaxUnits];  // staging units
   uint64_t dwfull, dwempty, wready, drain;
   uint32_t tmem_base;
+  uint32_t last;  // this CTA finished last of its column block
   volatile int abort_flag;
 };
 
 struct Params {
   const __nv_bfloat16* Wg;
   const uint8_t* mask;
-  float* dw;       // [ranges, d, E]
-  int32_t* err;
+  RouteSums sums;
   int T, d, E, stride, cols, ranges, tiles;
   int want_dx, want_dw, add;
 };
 
 __device__ __forceinline__ void give_up(const Params& p, Ctl& c, int code) {
-  if (!c.abort_flag) atomicOr(p.err, code);
+  if (!c.abort_flag) atomicOr(p.sums.err, code);
   c.abort_flag = 1;
 }
 
@@ -161,26 +161,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem_base;
-  pdl_wait();
+  // This kernel may start once every CTA of the dz kernel is past its own
+  // pdl_wait, so all that came before that one is done: x, W_g and dx_acc are
+  // read at once, and only what the dz kernel writes waits for its end.
   pdl_trigger();
 
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------ TMA loads
+      const int nx = p.want_dw ? halves : 0;
+      auto load_x = [&](int i, int stage) {
+        const uint32_t bar = smem_u32(&c.full[stage]);
+        mbar_arrive_expect_tx(bar, (nx + NB) * kUnit);
+        for (int h = 0; h < nx; ++h)
+          tma_load_2d(base + stage * C::STAGE + h * kUnit, &tmX, bar, c0 + 64 * h,
+                      (tile0 + i) * kRbTcTokens);
+      };
+      const int early = min(C::STAGES, ntiles);
+      for (int i = 0; i < early; ++i) load_x(i, i);
+      pdl_wait();
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       for (int i = 0; i < ntiles; ++i) {
-        if (c.abort_flag || !mbar_wait(smem_u32(&c.empty[stage]), phase ^ 1)) {
-          give_up(p, c, kErrTimeoutProducer);
-          break;
+        if (i >= early) {
+          if (c.abort_flag || !mbar_wait(smem_u32(&c.empty[stage]), phase ^ 1)) {
+            give_up(p, c, kErrTimeoutProducer);
+            break;
+          }
+          load_x(i, stage);
         }
-        const uint32_t bar = smem_u32(&c.full[stage]);
-        const uint32_t dst = base + stage * C::STAGE;
-        const int row = (tile0 + i) * kRbTcTokens;
-        const int nx = p.want_dw ? halves : 0;
-        mbar_arrive_expect_tx(bar, (nx + NB) * kUnit);
-        for (int h = 0; h < nx; ++h) tma_load_2d(dst + h * kUnit, &tmX, bar, c0 + 64 * h, row);
-        for (int b = 0; b < NB; ++b) tma_load_2d(dst + (2 + b) * kUnit, &tmDz, bar, 64 * b, row);
+        for (int b = 0; b < NB; ++b)
+          tma_load_2d(base + stage * C::STAGE + (2 + b) * kUnit, &tmDz, smem_u32(&c.full[stage]),
+                      64 * b, (tile0 + i) * kRbTcTokens);
         ++issued;
         if (++stage == C::STAGES) stage = 0, phase ^= 1;
       }
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; ok && i < ntiles; ++i) {
         const int buf = i & 1;
         ok = !c.abort_flag &&
-             mbar_wait(smem_u32(p.mask ? &c.clean[stage] : &c.full[stage]), phase) &&
+             mbar_wait(smem_u32(&c.full[stage]), phase) &&
              (!p.want_dx || mbar_wait(smem_u32(&c.tempty[buf]), ((i >> 1) & 1) ^ 1));
         if (!ok) {
           give_up(p, c, kErrTimeoutMma);
@@ -226,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (p.want_dw) {
           const bool first = i % kFlush == 0;
-          if (first && i > 0 && !mbar_wait(smem_u32(&c.dwempty), (flushed++) & 1)) {
+          if ((first && i > 0 && !mbar_wait(smem_u32(&c.dwempty), (flushed++) & 1)) ||
+              (p.mask && !mbar_wait(smem_u32(&c.clean[stage]), phase))) {
             give_up(p, c, kErrTimeoutMma);
             break;
           }
@@ -264,7 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     c0 + 64 * (u % halves), (tile0 + u / halves) * kRbTcTokens);
       };
       int readied = 0;
-      for (; readied < C::UNITS && readied < units; ++readied) make_ready(readied);
+      // The epilogue lays W_g out by way of the first unit.
+      const bool laid = mbar_wait(smem_u32(&c.wready), 0);
+      if (!laid) give_up(p, c, kErrTimeoutEpilogue);
+      for (; laid && readied < C::UNITS && readied < units; ++readied) make_ready(readied);
       for (int u = 0; u < units; ++u) {
         const int slot = u % C::UNITS;
         if (c.abort_flag || !mbar_wait(smem_u32(&c.ustaged[slot]), (u / C::UNITS) & 1)) {
@@ -274,8 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_store_2d(&tmDx, base + C::OUT_OFF + slot * kUnit, c0 + 64 * (u % halves),
                      (tile0 + u / halves) * kRbTcTokens);
         bulk_commit();
-        if (readied < units) {
-          bulk_wait_read<0>();
+        // The unit before has left its place by now, or nearly.
+        if (u > 0 && readied < units) {
+          bulk_wait_read<1>();
           make_ready(readied++);
         }
       }
@@ -289,55 +306,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------- rows of padding tokens
     int stage = 0;
     uint32_t phase = 0;
+    // Bit r of lane l's word q: row 32 q + l of the tile is padding.
+    auto padding = [&](int i) {
+      uint32_t bits = 0;
+      for (int q = 0; q < 4; ++q) {
+        const int t = (tile0 + i) * kRbTcTokens + 32 * q + lane;
+        if (t < p.T && !p.mask[t]) bits |= 1u << q;
+      }
+      return bits;
+    };
+    const bool scrub = p.mask && p.want_dw;
+    uint32_t bits = scrub ? padding(0) : 0;
     for (int i = 0; p.mask && i < ntiles; ++i) {
-      if (c.abort_flag || !mbar_wait(smem_u32(&c.full[stage]), phase)) {
+      const uint32_t next = scrub && i + 1 < ntiles ? padding(i + 1) : 0;
+      if (!__all_sync(0xffffffffu, !c.abort_flag && mbar_wait(smem_u32(&c.full[stage]), phase))) {
         give_up(p, c, kErrTimeoutMma);
         break;
       }
-      for (int r = lane; p.want_dw && r < kRbTcTokens; r += 32) {
-        const int t = (tile0 + i) * kRbTcTokens + r;
-        if (t >= p.T || p.mask[t]) continue;
-        for (int h = 0; h < halves; ++h)
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch)
-            *reinterpret_cast<uint4*>(smem + stage * C::STAGE + h * kUnit + r * 128 + ch * 16) =
-                make_uint4(0, 0, 0, 0);
+      for (int q = 0; q < 4; ++q) {
+        uint32_t rows = __ballot_sync(0xffffffffu, (bits >> q) & 1u);
+        while (rows) {  // two rows a turn, 16 bytes a lane
+          const int r0 = __ffs(rows) - 1;
+          rows &= rows - 1;
+          const int r1 = rows ? __ffs(rows) - 1 : r0;
+          rows &= rows - 1;
+          const int r = 32 * q + (lane < 16 ? r0 : r1);
+          *reinterpret_cast<uint4*>(smem + stage * C::STAGE + (lane & 8) / 8 * kUnit + r * 128 +
+                                    (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
       }
       fence_async_shared();
       mbar_arrive(smem_u32(&c.clean[stage]));
+      bits = next;
       if (++stage == C::STAGES) stage = 0, phase ^= 1;
+    }
+    if (p.sums.dbias) {
+      pdl_wait();
+      for (int e = blockIdx.x; e < p.E; e += gridDim.x) sum_bias(p.sums, e, lane);
     }
   } else {
     // --------------------------------------------------------- epilogue
     const int et = tid - 128, group = et >> 7, q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    {
+    if (p.want_dx) {
       // W_g of the block as the K-major operand: term after term, zero past
-      // the last expert and column.  Thread (row, group) makes half of a row.
-      const int col = c0 + row;
-      const __nv_bfloat16* w = p.Wg + static_cast<int64_t>(col) * p.E;
-      const bool in = p.want_dx && col < p.d;
-      constexpr int HALF = 32 * C::WB;
-      int e = NB == 3 ? group * HALF : group * HALF % p.stride;
-      int left = (NB == 3 ? p.E : 3 * p.stride) - group * HALF;  // elements that are not zero
+      // the last expert and column.  The block's rows are contiguous, so they
+      // come in 16-byte pieces into the first staging unit (dx_acc waits for
+      // wready) and are spread out from there.
+      uint8_t* raw = smem + C::OUT_OFF;
+      const int bytes = min(kRbTcCols, p.d - c0) * p.E * 2;  // columns come in eights
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(p.Wg + static_cast<int64_t>(c0) * p.E);
+      for (int i = et * 16; i < kUnit; i += kEpilogue * 16)
+        *reinterpret_cast<uint4*>(raw + i) =
+            i < bytes ? *reinterpret_cast<const uint4*>(from + i) : make_uint4(0, 0, 0, 0);
+      epilogue_sync();
+      const uint16_t* w = reinterpret_cast<const uint16_t*>(raw);
 #pragma unroll
-      for (int ch = 0; ch < HALF / 8; ++ch) {
+      for (int j = 0; j < 4 * C::WB; ++j) {
+        const int i = et + j * kEpilogue, r = i / (8 * C::WB), n = i % (8 * C::WB);
+        int e = NB == 3 ? 8 * n : 8 * n % p.stride;
+        int left = (NB == 3 ? p.E : 3 * p.stride) - 8 * n;  // elements that are not zero
         uint32_t v[4];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const uint32_t b =
-              in && left > 0 ? static_cast<uint32_t>(__bfloat16_as_ushort(w[e])) : 0u;
-          v[u / 2] = u % 2 ? v[u / 2] | (b << 16) : b;
-          --left;
+          const uint32_t x = left > u ? w[r * p.E + e] : 0u;
+          v[u / 2] = u % 2 ? v[u / 2] | (x << 16) : x;
           if (++e == p.stride) e = 0;
         }
-        const int n = group * HALF / 8 + ch;  // 16-byte chunk of the row
-        *reinterpret_cast<uint4*>(smem + C::W_OFF + n / 8 * kUnit + swz(row, n % 8)) =
+        *reinterpret_cast<uint4*>(smem + C::W_OFF + n / 8 * kUnit + swz(r, n % 8)) =
             make_uint4(v[0], v[1], v[2], v[3]);
       }
       fence_async_shared();
-      mbar_arrive(smem_u32(&c.wready));
     }
+    mbar_arrive(smem_u32(&c.wready));
     // dW_g so far: lane = column; 32 NB of the block's columns a thread, the
     // three terms of one expert already added where their places are known.
     constexpr int ACC = NB == 3 ? 32 : 32 * NB;
@@ -404,24 +445,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok) give_up(p, c, kErrTimeoutEpilogue);
-    if (p.want_dw && epilogue_all(ok)) {
-      // The last flush came after the last MMA: the ring is idle, and the
-      // rows go through it so that they leave in whole lines.
-      float* rows = reinterpret_cast<float*>(smem);
-      constexpr int LD = 2 * ACC + 1;
+    if (p.want_dw) {
+      if (epilogue_all(ok)) {
+        // The last flush came after the last MMA: the ring is idle, and the
+        // rows go through it so that they leave in whole lines.
+        float* rows = reinterpret_cast<float*>(smem);
+        constexpr int LD = 2 * ACC + 1;
 #pragma unroll
-      for (int e = 0; e < ACC; ++e) rows[row * LD + group * ACC + e] = acc[e];
+        for (int e = 0; e < ACC; ++e) rows[row * LD + group * ACC + e] = acc[e];
+        epilogue_sync();
+        const int n = min(kRbTcCols, p.d - c0) * p.E;
+        float* out = p.sums.dw + (static_cast<int64_t>(range) * p.d + c0) * p.E;
+        int r = et / p.E, e = et % p.E;
+        const int dr = kEpilogue / p.E, de = kEpilogue % p.E;
+        for (int i = et; i < n; i += kEpilogue) {
+          const float* at = rows + r * LD + e;
+          out[i] = NB == 3 ? at[0] : at[2 * p.stride] + at[p.stride] + at[0];
+          r += dr;
+          e += de;
+          if (e >= p.E) e -= p.E, ++r;
+        }
+      }
+      __threadfence();
       epilogue_sync();
-      const int n = min(kRbTcCols, p.d - c0) * p.E;
-      float* out = p.dw + (static_cast<int64_t>(range) * p.d + c0) * p.E;
-      int r = et / p.E, e = et % p.E;
-      const int dr = kEpilogue / p.E, de = kEpilogue % p.E;
-      for (int i = et; i < n; i += kEpilogue) {
-        const float* at = rows + r * LD + e;
-        out[i] = NB == 3 ? at[0] : at[2 * p.stride] + at[p.stride] + at[0];
-        r += dr;
-        e += de;
-        if (e >= p.E) e -= p.E, ++r;
+      if (et == 0)
+        c.last = atomicAdd(p.sums.tickets + blockIdx.x % p.cols, 1u) + 1 ==
+                 static_cast<uint32_t>(p.ranges);
+      epilogue_sync();
+      if (c.last) {
+        __threadfence();
+        sum_ranges(p.sums, c0, min(kRbTcCols, p.d - c0), et, kEpilogue);
       }
     }
   }
@@ -463,7 +516,7 @@ bool make_map(CUtensorMap* m, const void* at, uint64_t rows, uint64_t cols) {
 }  // namespace
 
 cudaError_t launch_route_products_tc(const RouteBackwardArgs& a, const RouteBackwardPlan& p,
-                                     cudaStream_t s) {
+                                     const RouteSums& sums, cudaStream_t s) {
   const DzTerms t = dz_terms(a.E);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   CUtensorMap mx, mdz, macc, mdx;
@@ -475,8 +528,7 @@ cudaError_t launch_route_products_tc(const RouteBackwardArgs& a, const RouteBack
     return cudaErrorInvalidValue;
   Params k{static_cast<const __nv_bfloat16*>(a.Wg),
            a.mask,
-           reinterpret_cast<float*>(ws + p.dw),
-           reinterpret_cast<int32_t*>(ws + p.err),
+           sums,
            a.T,
            a.d,
            a.E,
