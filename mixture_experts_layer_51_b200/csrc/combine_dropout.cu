@@ -51,18 +51,35 @@ __device__ __forceinline__ void store8(void* y, int64_t row, int d, int c8, cons
   }
 }
 
-// Warps of a CTA sharing one token's row (1, 2, 4 or 8), a lane's first
-// 8-element chunk and the stride between its chunks.
+// Warps of a CTA sharing one token's row (1, 2, 4 or 8): this warp's token,
+// and which of the token's warps it is.
 struct Place {
-  int t, c0, step;
+  int t, part;
 };
 __device__ __forceinline__ Place place(int wpt) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  return {static_cast<int>(blockIdx.x) * (kCdWarps / wpt) + warp / wpt,
-          (warp % wpt) * 32 + lane, wpt * 32};
+  const int warp = threadIdx.x >> 5;
+  return {static_cast<int>(blockIdx.x) * (kCdWarps / wpt) + warp / wpt, warp % wpt};
 }
 
-template <bool BF16>
+// The token's rows and gates, in every lane (row -1: no such slot).
+template <int KJ>
+__device__ __forceinline__ void slots(const int32_t* pos, const float* gate, int64_t t, int k,
+                                      int (&row)[KJ], float (&g)[KJ]) {
+  const int lane = threadIdx.x & 31;
+  const int pl = lane < k ? pos[t * k + lane] : -1;
+  const float gl = lane < k ? gate[t * k + lane] : 0.f;
+#pragma unroll
+  for (int j = 0; j < KJ; ++j) {
+    row[j] = __shfl_sync(0xffffffffu, pl, j);
+    g[j] = __shfl_sync(0xffffffffu, gl, j);
+  }
+}
+
+// KJ = slots this instantiation handles (2 for k <= 2, else kMaxK); CH =
+// 8-element chunks of each row per lane and iteration: every load of an
+// iteration is issued before any arithmetic (the generator's, too, runs while
+// they are on their way).
+template <bool BF16, int KJ, int CH>
 __global__ void __launch_bounds__(kCdWarps * 32)
     combine_dropout_kernel(const void* __restrict__ o, const int32_t* __restrict__ pos,
                            const float* __restrict__ gate, const void* residual,
@@ -73,33 +90,72 @@ __global__ void __launch_bounds__(kCdWarps * 32)
   const Place at = place(wpt);
   if (at.t >= T) return;
   const int64_t t = at.t;
-  const int n8 = d / 8;
+  const int n8 = d / 8, lane = threadIdx.x & 31;
   uint64_t seed = 0, offset = 0;
   if (threshold) seed = rng[0], offset = rng[1];
-  for (int c8 = at.c0; c8 < n8; c8 += at.step) {
-    float acc[8] = {};
-    for (int j = 0; j < k; ++j) {
-      const int p = pos[t * k + j];
-      if (p < 0) continue;
-      Row8<BF16> v;
-      v.load(o, p, d, c8);
-      v.fma_into(gate[t * k + j], acc);
-    }
-    if (threshold) {
-      const uint32_t keep = dropout_keep8(t * n8 + c8, offset, seed, threshold);
+  int row[KJ];
+  float g[KJ];
+  slots<KJ>(pos, gate, t, k, row, g);
+  for (int c0 = at.part * 32 * CH + lane; c0 < n8; c0 += wpt * 32 * CH) {
+    Row8<BF16> v[KJ][CH], res[CH];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = (keep >> i) & 1u ? acc[i] * scale : 0.f;
+    for (int h = 0; h < CH; ++h) {
+      const int c8 = c0 + h * 32;
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) {
+        if (row[j] >= 0 && c8 < n8)
+          v[j][h].load(o, row[j], d, c8);
+        else
+          v[j][h].zero();
+      }
+      if (residual && c8 < n8)
+        res[h].load(residual, t, d, c8);
+      else
+        res[h].zero();
     }
-    if (residual) {
-      Row8<BF16> r;
-      r.load(residual, t, d, c8);
-      r.fma_into(1.f, acc);
+#pragma unroll
+    for (int h = 0; h < CH; ++h) {
+      const int c8 = c0 + h * 32;
+      if (c8 >= n8) break;
+      uint32_t w[4];
+      if (threshold) philox4x32_10(t * n8 + c8, offset, seed, w);
+      float acc[8] = {};
+#pragma unroll
+      for (int j = 0; j < KJ; ++j)
+        if (row[j] >= 0) v[j][h].fma_into(g[j], acc);  // absent slots add nothing
+      if (threshold) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = dropout_kept(w, i, threshold) ? acc[i] * scale : 0.f;
+      }
+      if (residual) res[h].fma_into(1.f, acc);
+      store8<BF16>(y, t, d, c8, acc);
     }
-    store8<BF16>(y, t, d, c8, acc);
   }
 }
 
-template <bool BF16>
+// Adds `v` over the 32 lanes: afterwards lane l holds in the result the total
+// of v[l / (32 / N) % N], each added in an order that is always the same.
+template <int N>
+__device__ __forceinline__ float reduce_lanes(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int s = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2, s /= 2) {
+    // The upper half of the lanes keeps the upper half of the values.
+    const bool upper = lane & s;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = upper ? v[i] : v[i + n];
+      const float keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+    }
+  }
+#pragma unroll
+  for (; s > 0; s /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
+  return v[0];
+}
+
+template <bool BF16, int KJ, int CH>
 __global__ void __launch_bounds__(kCdWarps * 32)
     combine_dropout_backward_kernel(const void* __restrict__ dy, const void* __restrict__ o,
                                     const int32_t* __restrict__ pos,
@@ -107,60 +163,84 @@ __global__ void __launch_bounds__(kCdWarps * 32)
                                     const uint64_t* __restrict__ rng, uint32_t threshold,
                                     float scale, int T, int d, int k, int wpt,
                                     void* __restrict__ d_o, float* __restrict__ dgate) {
-  __shared__ float part[kCdWarps][kMaxK];
+  __shared__ float part[kCdWarps][KJ];
   pdl_wait();
   pdl_trigger();
   const Place at = place(wpt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = at.t;
   const int n8 = d / 8;
-  float dot[kMaxK] = {};
+  float dot[KJ] = {};
+  int row[KJ];
+#pragma unroll
+  for (int j = 0; j < KJ; ++j) row[j] = -1;
   if (at.t < T) {
+    float g[KJ];
     uint64_t seed = 0, offset = 0;
     if (threshold) seed = rng[0], offset = rng[1];
-    for (int c8 = at.c0; c8 < n8; c8 += at.step) {
-      Row8<BF16> r;
-      float a[8];
-      r.load(dy, t, d, c8);
-      unpack8(r, a);
-      uint32_t keep = 0xffu;
-      if (threshold) {
-        keep = dropout_keep8(t * n8 + c8, offset, seed, threshold);
+    slots<KJ>(pos, gate, t, k, row, g);
+    for (int c0 = at.part * 32 * CH + lane; c0 < n8; c0 += wpt * 32 * CH) {
+      Row8<BF16> v[KJ][CH], up[CH];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = (keep >> i) & 1u ? a[i] * scale : 0.f;
+      for (int h = 0; h < CH; ++h) {
+        const int c8 = c0 + h * 32;
+        if (c8 >= n8) break;
+        up[h].load(dy, t, d, c8);
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+          if (row[j] >= 0) v[j][h].load(o, row[j], d, c8);
       }
 #pragma unroll
-      for (int j = 0; j < kMaxK; ++j) {
-        const int p = j < k ? pos[t * k + j] : -1;
-        if (p < 0) continue;
-        float v[8];
-        r.load(o, p, d, c8);
-        unpack8(r, v);
-        const float g = gate[t * k + j];
+      for (int h = 0; h < CH; ++h) {
+        const int c8 = c0 + h * 32;
+        if (c8 >= n8) break;
+        float a[8];
+        bool kept[8];
+        uint32_t w[4];
+        if (threshold) philox4x32_10(t * n8 + c8, offset, seed, w);
+        unpack8(up[h], a);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if ((keep >> i) & 1u) dot[j] = fmaf(a[i], v[i], dot[j]);
-          v[i] = (keep >> i) & 1u ? g * a[i] : 0.f;
+          kept[i] = !threshold || dropout_kept(w, i, threshold);
+          a[i] = kept[i] ? a[i] * scale : 0.f;
         }
-        store8<BF16>(d_o, p, d, c8, v);
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+          if (row[j] < 0) continue;
+          float f[8];
+          unpack8(v[j][h], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // a is 0 where the element was dropped; what o holds there is
+            // left out, since 0 times it need not be 0.
+            dot[j] = fmaf(a[i], kept[i] ? f[i] : 0.f, dot[j]);
+            f[i] = g[j] * a[i];
+          }
+          store8<BF16>(d_o, row[j], d, c8, f);
+        }
       }
     }
   }
   // The row's dot products: over the lanes, then over the warps that share it.
-#pragma unroll
-  for (int j = 0; j < kMaxK; ++j) {
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
-    if (lane == 0) part[warp][j] = dot[j];
+  const float sum = reduce_lanes<KJ>(dot);
+  constexpr int W = 32 / KJ;  // lanes that hold the same total
+  if (wpt == 1) {
+    if (at.t < T && lane % W == 0 && lane / W < k)
+      dgate[t * k + lane / W] = pos[t * k + lane / W] >= 0 ? sum : 0.f;
+    return;
   }
+  if (lane % W == 0) part[warp][lane / W] = sum;
   __syncthreads();
-  if (at.t < T && warp % wpt == 0 && lane < k) {
-    float sum = 0.f;
-    for (int w = 0; w < wpt; ++w) sum += part[warp + w][lane];
-    dgate[t * k + lane] = pos[t * k + lane] >= 0 ? sum : 0.f;
+  if (at.t < T && at.part == 0 && lane < k) {
+    float total = 0.f;
+    for (int i = 0; i < wpt; ++i) total += part[warp + i][lane];
+    dgate[t * k + lane] = pos[t * k + lane] >= 0 ? total : 0.f;
   }
 }
 
+// Warps a token: one where the tokens alone fill the GPU (eight warps on each
+// of 148 SMs), else as many as it takes, while each keeps a whole sweep of a
+// row (256 elements) to itself.
 int warps_per_token(int T, int d) {
   int wpt = 1;
   while (wpt < kCdWarps && static_cast<int64_t>(T) * wpt < 148 * kCdWarps && wpt * 256 < d) wpt *= 2;
@@ -176,7 +256,11 @@ cudaError_t launch_combine_dropout(const CombineDropoutArgs& a, moe_dtype dtype,
     return launch_kernel(kern, grid, dim3(kCdWarps * 32), 0, s, 1, true, a.o, a.pos, a.gate,
                          a.residual, a.rng, a.threshold, a.scale, a.T, a.d, a.k, wpt, a.y);
   };
-  return dtype == MOE_BF16 ? go(combine_dropout_kernel<true>) : go(combine_dropout_kernel<false>);
+  if (dtype == MOE_BF16)
+    return a.k <= 2 ? go(combine_dropout_kernel<true, 2, 4>)
+                    : go(combine_dropout_kernel<true, kMaxK, 2>);
+  return a.k <= 2 ? go(combine_dropout_kernel<false, 2, 2>)
+                  : go(combine_dropout_kernel<false, kMaxK, 1>);
 }
 
 cudaError_t launch_combine_dropout_backward(const CombineDropoutArgs& a, moe_dtype dtype,
@@ -187,8 +271,11 @@ cudaError_t launch_combine_dropout_backward(const CombineDropoutArgs& a, moe_dty
     return launch_kernel(kern, grid, dim3(kCdWarps * 32), 0, s, 1, true, a.dy, a.o, a.pos, a.gate,
                          a.rng, a.threshold, a.scale, a.T, a.d, a.k, wpt, a.d_o, a.dgate);
   };
-  return dtype == MOE_BF16 ? go(combine_dropout_backward_kernel<true>)
-                           : go(combine_dropout_backward_kernel<false>);
+  if (dtype == MOE_BF16)
+    return a.k <= 2 ? go(combine_dropout_backward_kernel<true, 2, 2>)
+                    : go(combine_dropout_backward_kernel<true, kMaxK, 1>);
+  return a.k <= 2 ? go(combine_dropout_backward_kernel<false, 2, 1>)
+                  : go(combine_dropout_backward_kernel<false, kMaxK, 1>);
 }
 
 }  // namespace moe

@@ -34,20 +34,25 @@ __host__ __device__ __forceinline__ void philox4x32_10(uint64_t n, uint64_t offs
   }
 }
 
-// Dropout's decision for eight consecutive elements (element group n): bit i
-// is set where element 8 n + i is kept.  16 random bits an element, so one
-// call covers a 16-byte vector of bf16 and the drop probability is a multiple
-// of 2^-16: dropped below `threshold` (0 .. 65535).
+// Dropout's decision for eight consecutive elements (element group n) from the
+// words of counter n: element 8 n + i takes the low (even i) or high half of
+// word i / 2 and is dropped below `threshold` (0 .. 65535).  16 random bits an
+// element, so one call covers a 16-byte vector of bf16 and the drop
+// probability is a multiple of 2^-16.
+__host__ __device__ __forceinline__ bool dropout_kept(const uint32_t (&w)[4], int i,
+                                                      uint32_t threshold) {
+  const uint32_t high = i % 2 ? w[i / 2] : w[i / 2] << 16;  // the low half below plays no part
+  return high >= threshold << 16;
+}
+
+// All eight: bit i is set where element 8 n + i is kept.
 __host__ __device__ __forceinline__ uint32_t dropout_keep8(uint64_t n, uint64_t offset,
                                                            uint64_t seed, uint32_t threshold) {
   uint32_t w[4];
   philox4x32_10(n, offset, seed, w);
   uint32_t keep = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    keep |= ((w[i] & 0xffffu) >= threshold ? 1u : 0u) << (2 * i);
-    keep |= ((w[i] >> 16) >= threshold ? 1u : 0u) << (2 * i + 1);
-  }
+  for (int i = 0; i < 8; ++i) keep |= (dropout_kept(w, i, threshold) ? 1u : 0u) << i;
   return keep;
 }
 
