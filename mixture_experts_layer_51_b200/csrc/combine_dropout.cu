@@ -179,6 +179,8 @@ __global__ void __launch_bounds__(kCdWarps * 32)
     uint64_t seed = 0, offset = 0;
     if (threshold) seed = rng[0], offset = rng[1];
     slots<KJ>(pos, gate, t, k, row, g);
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) g[j] *= scale;
     for (int c0 = at.part * 32 * CH + lane; c0 < n8; c0 += wpt * 32 * CH) {
       Row8<BF16> v[KJ][CH], up[CH];
 #pragma unroll
@@ -194,27 +196,27 @@ __global__ void __launch_bounds__(kCdWarps * 32)
       for (int h = 0; h < CH; ++h) {
         const int c8 = c0 + h * 32;
         if (c8 >= n8) break;
-        float a[8];
-        bool kept[8];
-        uint32_t w[4];
-        if (threshold) philox4x32_10(t * n8 + c8, offset, seed, w);
-        unpack8(up[h], a);
+        // Dropped elements become zero in dy and in o (what o holds there is
+        // left out: 0 times it need not be 0), halfword masks for both.
+        uint32_t m[4];
+        if (threshold) {
+          philox4x32_10(t * n8 + c8, offset, seed, m);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          kept[i] = !threshold || dropout_kept(w, i, threshold);
-          a[i] = kept[i] ? a[i] * scale : 0.f;
+          for (int i = 0; i < 4; ++i) m[i] = __vcmpgeu2(m[i], threshold << 16 | threshold);
+          up[h].mask(m);
         }
+        float a[8];
+        unpack8(up[h], a);
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
           if (row[j] < 0) continue;
+          if (threshold) v[j][h].mask(m);
           float f[8];
           unpack8(v[j][h], f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            // a is 0 where the element was dropped; what o holds there is
-            // left out, since 0 times it need not be 0.
-            dot[j] = fmaf(a[i], kept[i] ? f[i] : 0.f, dot[j]);
-            f[i] = g[j] * a[i];
+            dot[j] = fmaf(a[i], f[i], dot[j]);
+            f[i] = g[j] * a[i];  // g carries the scale
           }
           store8<BF16>(d_o, row[j], d, c8, f);
         }
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kCdWarps * 32)
     }
   }
   // The row's dot products: over the lanes, then over the warps that share it.
-  const float sum = reduce_lanes<KJ>(dot);
+  const float sum = scale * reduce_lanes<KJ>(dot);
   constexpr int W = 32 / KJ;  // lanes that hold the same total
   if (wpt == 1) {
     if (at.t < T && lane % W == 0 && lane / W < k)
