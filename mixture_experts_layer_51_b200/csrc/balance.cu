@@ -3,32 +3,31 @@
 //     counts_e = #{(t, j) : idx_tj = e},  S_e = sum_t p_te,  N = #{t}
 //     L = coef E sum_e (counts_e / (N k)) (S_e / N)
 //
-// over the counted tokens t (all, or those the mask names).  Two launches:
-// every CTA sums a slice of the tokens for all experts, then one CTA adds the
-// slices in order (no floating-point atomics: the sums do not depend on
-// scheduling).  Bound by reading the scores once; small batches by the
-// launches.
+// over the counted tokens t (all, or those the mask names).  Every CTA sums a
+// slice of the tokens for all experts; the slices are added in order (no
+// floating-point atomics: the sums do not depend on scheduling).
+//
+// Bound by reading the scores once, and for small batches by launches and
+// round trips to memory.  So there are two forms.  A batch of up to 1 MB is
+// one launch: a cluster of eight CTAs whose first adds the others' sums out
+// of their shared memory.  A larger one takes a CTA on every SM, and a second
+// launch adds the slices from the workspace.
+// MEASURED
 
 #include "moe_internal.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kBlThreads = 512;
-constexpr int kBlWarps = kBlThreads / 32;
-constexpr int kBlMaxSlices = 296;   // two CTAs on each of 148 SMs
-constexpr int kBlMinSlice = 256;    // tokens
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int64_t kClusterBytes = 1 << 20;
+constexpr int kMaxSlices = 148;     // one CTA on each SM
+constexpr int kMinSlice = 256;      // tokens
+constexpr int kBatch = 8;           // scores a lane has on their way per expert
 
-struct Slices {
-  int n, len;  // slices, tokens in each (a multiple of 32; the last may hold fewer)
-};
-Slices slices(int T) {
-  const int64_t per = (static_cast<int64_t>(T) + kBlMaxSlices - 1) / kBlMaxSlices;
-  int64_t len = per < kBlMinSlice ? kBlMinSlice : (per + 31) / 32 * 32;
-  return {static_cast<int>((T + len - 1) / len), static_cast<int>(len)};
-}
-
-// A slice's sums in the workspace: S_e, counts_e, N.
+// A slice's sums: S_e, counts_e, N.
 struct Partial {
   float sum[kMaxE];
   int32_t count[kMaxE];
@@ -36,70 +35,175 @@ struct Partial {
   int32_t pad[3];
 };
 
-__global__ void __launch_bounds__(kBlThreads)
-    balance_slice_kernel(const float* __restrict__ scores, const int32_t* __restrict__ idx,
-                         const uint8_t* __restrict__ mask, int T, int E, int k, int len,
-                         Partial* __restrict__ out) {
-  __shared__ int32_t cnt[kMaxE];
-  __shared__ int32_t ntok;
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t0 = blockIdx.x * len, t1 = min(T, t0 + len);
-  if (tid < kMaxE) cnt[tid] = 0;
-  if (tid == 0) ntok = 0;
-  __syncthreads();
-  for (int t = t0 + tid; t < t1; t += kBlThreads) {
-    if (mask && !mask[t]) continue;
-    atomicAdd(&ntok, 1);
-    for (int j = 0; j < k; ++j) {
-      const int e = idx[static_cast<int64_t>(t) * k + j];
-      if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
-    }
-  }
-  Partial& p = out[blockIdx.x];
-  for (int e = warp; e < E; e += kBlWarps) {
-    float s = 0.f;
-    for (int t = t0 + lane; t < t1; t += 32)
-      if (!mask || mask[t]) s += scores[static_cast<int64_t>(e) * T + t];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) p.sum[e] = s;
-  }
-  __syncthreads();
-  if (tid < E) p.count[tid] = cnt[tid];
-  if (tid == 0) p.tokens = ntok;
+struct Slices {
+  int n, len;  // slices, tokens in each (a multiple of 32; the last may hold fewer)
+};
+bool one_cluster(int T, int E, int k) {
+  return static_cast<int64_t>(T) * (E + k) * 4 <= kClusterBytes;
+}
+Slices slices(int T) {
+  const int64_t per = (static_cast<int64_t>(T) + kMaxSlices - 1) / kMaxSlices;
+  const int64_t len = per < kMinSlice ? kMinSlice : (per + 31) / 32 * 32;
+  return {static_cast<int>((T + len - 1) / len), static_cast<int>(len)};
 }
 
-__global__ void __launch_bounds__(kMaxE)
-    balance_finish_kernel(const Partial* __restrict__ part, int n, int E, int k, float coef,
-                          float* __restrict__ loss, float* __restrict__ prob_sum,
-                          int32_t* __restrict__ counts, int32_t* __restrict__ tokens) {
-  __shared__ double term[kMaxE];
+// The sums over tokens t0 .. t1 - 1 into `out` (shared memory), by the whole
+// CTA.  A warp takes an expert's scores, 256 tokens at a time; with fewer
+// than 32 experts several warps share one, each with a part of the tokens.
+__device__ void sum_slice(const float* __restrict__ scores, const int32_t* __restrict__ idx,
+                          const uint8_t* __restrict__ mask, int T, int E, int k, uint32_t t0,
+                          uint32_t t1, Partial& out) {
+  __shared__ float part[kWarps][2];  // a warp's experts: at most two
+  __shared__ int32_t count_s[kMaxE];
+  __shared__ int32_t tokens_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid < kMaxE) count_s[tid] = 0;
+  if (tid == kMaxE) tokens_s = 0;
+  // Experts of a round of warps (a power of two), and warps to an expert.
+  const int wide = E > 16 ? 32 : E > 8 ? 16 : E > 4 ? 8 : E > 2 ? 4 : E;
+  const int share = kWarps / wide, e0 = warp % wide, q = warp / wide;
+  float s[2] = {0.f, 0.f};
+  for (uint32_t t = t0 + q * 32 * kBatch + lane; t < t1; t += share * 32 * kBatch) {
+    float v[2][kBatch];
+    uint32_t on = 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const uint32_t at = t + 32 * i;
+      const bool in = at < t1;
+      if (in && (!mask || mask[at])) on |= 1u << i;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = e0 + h * wide;
+        v[h][i] = in && e < E ? __ldg(scores + static_cast<int64_t>(e) * T + at) : 0.f;
+      }
+    }
+    // A token that does not count may hold anything: left out, not times 0.
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) s[h] += on >> i & 1u ? v[h][i] : 0.f;
+  }
+  __syncthreads();  // the counters are zero
+  for (uint32_t t = t0 + tid; t - lane < t1; t += kThreads) {
+    const bool counted = t < t1 && (!mask || mask[t]);
+    const unsigned any = __ballot_sync(0xffffffffu, counted);
+    if (lane == 0 && any) atomicAdd(&tokens_s, __popc(any));
+    int sel[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      sel[j] = counted && j < k ? __ldg(idx + static_cast<int64_t>(t) * k + j) : -1;
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (sel[j] >= 0 && sel[j] < E) atomicAdd(&count_s[sel[j]], 1);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], o);
+    if (lane == 0) part[warp][h] = s[h];
+  }
+  __syncthreads();
+  if (tid < kMaxE) {
+    float total = 0.f;
+    if (tid < E)
+      for (int i = 0; i < share; ++i) total += part[tid % wide + i * wide][tid / wide];
+    out.sum[tid] = total;
+    out.count[tid] = count_s[tid];
+  }
+  if (tid == kMaxE) out.tokens = tokens_s;
+}
+
+// The loss from the totals, by the first two warps (thread e: expert e).
+__device__ __forceinline__ void finish(int e, int E, int k, float coef, float sum, int32_t count,
+                                       int32_t tokens, const BalanceArgs& a) {
+  __shared__ double half;
+  double term = 0.0;
+  if (e < E) {
+    a.prob_sum[e] = sum;
+    a.counts[e] = count;
+    if (tokens > 0) term = static_cast<double>(count) / k * sum / tokens / tokens;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
+  if (e == 32) half = term;
+  asm volatile("bar.sync 1, 64;" ::: "memory");
+  if (e == 0) {
+    *a.loss = static_cast<float>(coef * E * (term + half));
+    *a.tokens = tokens;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) balance_cluster_kernel(const BalanceArgs a, int len) {
+  __shared__ Partial mine;
+  const int tid = threadIdx.x;
+  const uint32_t rank = cluster_ctarank();
   pdl_wait();
   pdl_trigger();
-  const int e = threadIdx.x;
-  float sum = 0.f;
-  int32_t count = 0, tok = 0;
-  for (int s = 0; s < n; ++s) {
-    if (e < E) {
-      sum += part[s].sum[e];
-      count += part[s].count[e];
+  const int t0 = min(a.T, static_cast<int>(rank) * len), t1 = min(a.T, t0 + len);
+  sum_slice(a.scores, a.idx, a.mask, a.T, a.E, a.k, t0, t1, mine);
+  cluster_sync();
+  if (rank == 0 && tid < kMaxE) {
+    float sum = 0.f;
+    int32_t count = 0, tokens = 0;
+    uint32_t v[kCluster][3];
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+      const uint32_t from = mapa_shared(smem_u32(&mine), r);
+      v[r][0] = ld_shared_cluster_u32(from + offsetof(Partial, sum) + 4 * tid);
+      v[r][1] = ld_shared_cluster_u32(from + offsetof(Partial, count) + 4 * tid);
+      v[r][2] = ld_shared_cluster_u32(from + offsetof(Partial, tokens));
     }
-    tok += part[s].tokens;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+      sum += __uint_as_float(v[r][0]);
+      count += static_cast<int32_t>(v[r][1]);
+      tokens += static_cast<int32_t>(v[r][2]);
+    }
+    finish(tid, a.E, a.k, a.coef, sum, count, tokens, a);
   }
-  if (e < E) {
-    prob_sum[e] = sum;
-    counts[e] = count;
-  }
-  term[e] = e < E && tok > 0 ? static_cast<double>(count) / k * sum / tok / tok : 0.0;
+  cluster_sync();  // the others' shared memory lives until it has been read
+}
+
+__global__ void __launch_bounds__(kThreads, 1) balance_slice_kernel(const BalanceArgs a, int len) {
+  __shared__ Partial mine;
+  pdl_wait();
+  pdl_trigger();
+  const int t0 = blockIdx.x * len, t1 = a.T - t0 < len ? a.T : t0 + len;
+  sum_slice(a.scores, a.idx, a.mask, a.T, a.E, a.k, t0, t1, mine);
   __syncthreads();
-  if (e == 0) {
-    double total = 0.0;
-    for (int i = 0; i < E; ++i) total += term[i];
-    *loss = static_cast<float>(coef * E * total);
-    *tokens = tok;
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(&mine);
+  uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<Partial*>(a.ws) + blockIdx.x);
+  for (int i = threadIdx.x; i < static_cast<int>(offsetof(Partial, pad)) / 4; i += kThreads)
+    to[i] = from[i];
+}
+
+__global__ void __launch_bounds__(kThreads, 1) balance_finish_kernel(const BalanceArgs a, int n) {
+  constexpr int G = kThreads / kMaxE;  // threads to an expert
+  __shared__ float sum_s[G][kMaxE];
+  __shared__ int32_t count_s[G][kMaxE], tokens_s[G];
+  pdl_wait();
+  pdl_trigger();
+  const int e = threadIdx.x % kMaxE, g = threadIdx.x / kMaxE;
+  const Partial* part = static_cast<const Partial*>(a.ws);
+  float sum = 0.f;
+  int32_t count = 0, tokens = 0;
+#pragma unroll 5
+  for (int s = g; s < n; s += G) {
+    sum += part[s].sum[e];
+    count += part[s].count[e];
+    tokens += part[s].tokens;
   }
+  sum_s[g][e] = sum;
+  count_s[g][e] = count;
+  if (e == 0) tokens_s[g] = tokens;
+  __syncthreads();
+  if (g > 0) return;
+  for (int i = 1; i < G; ++i) {
+    sum += sum_s[i][e];
+    count += count_s[i][e];
+    tokens += tokens_s[i];
+  }
+  finish(e, a.E, a.k, a.coef, sum, count, tokens, a);
 }
 
 }  // namespace
@@ -107,17 +211,16 @@ __global__ void __launch_bounds__(kMaxE)
 size_t balance_scratch_bytes(int T) { return sizeof(Partial) * (slices(T).n + 1); }
 
 cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
-  const Slices sl = slices(a.T);
-  Partial* part = static_cast<Partial*>(a.ws);
-  if (sl.n > 0) {
-    const cudaError_t err =
-        launch_kernel(balance_slice_kernel, dim3(sl.n), dim3(kBlThreads), 0, s, 1, true, a.scores,
-                      a.idx, a.mask, a.T, a.E, a.k, sl.len, part);
-    if (err != cudaSuccess) return err;
+  if (one_cluster(a.T, a.E, a.k)) {
+    const int len = (a.T + 32 * kCluster - 1) / (32 * kCluster) * 32;
+    return launch_kernel(balance_cluster_kernel, dim3(kCluster), dim3(kThreads), 0, s, kCluster,
+                         true, a, len);
   }
-  return launch_kernel(balance_finish_kernel, dim3(1), dim3(kMaxE), 0, s, 1, true,
-                       static_cast<const Partial*>(part), sl.n, a.E, a.k, a.coef, a.loss,
-                       a.prob_sum, a.counts, a.tokens);
+  const Slices sl = slices(a.T);
+  const cudaError_t err = launch_kernel(balance_slice_kernel, dim3(sl.n), dim3(kThreads), 0, s, 1,
+                                        true, a, sl.len);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(balance_finish_kernel, dim3(1), dim3(kThreads), 0, s, 1, true, a, sl.n);
 }
 
 }  // namespace moe

@@ -22,32 +22,77 @@ namespace {
 
 constexpr int kCdWarps = 8;
 
-__device__ __forceinline__ void unpack8(const Row8<true>& r, float (&f)[8]) {
-  const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+// Eight consecutive elements: their bytes, as loaded and stored (streaming:
+// each row is read once), and in fp32.
+template <bool BF16>
+struct Chunk;
+template <>
+struct Chunk<true> {
+  static constexpr int kBytes = 16;
+  uint4 v;
+  __device__ __forceinline__ void load(const char* p) {
+    v = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  // Elements 2 i and 2 i + 1 stay where the low and high half of m[i] are all
+  // ones, and become zero where they are zeros.
+  __device__ __forceinline__ void mask(const uint32_t (&m)[4]) {
+    v.x &= m[0], v.y &= m[1], v.z &= m[2], v.w &= m[3];
+  }
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(char* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                   pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Chunk<false> {
+  static constexpr int kBytes = 32;
+  float4 a, b;
+  __device__ __forceinline__ void load(const char* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void mask(const uint32_t (&m)[4]) {
+    a.x = m[0] & 1u ? a.x : 0.f;
+    a.y = m[0] >> 31 ? a.y : 0.f;
+    a.z = m[1] & 1u ? a.z : 0.f;
+    a.w = m[1] >> 31 ? a.w : 0.f;
+    b.x = m[2] & 1u ? b.x : 0.f;
+    b.y = m[2] >> 31 ? b.y : 0.f;
+    b.z = m[3] & 1u ? b.z : 0.f;
+    b.w = m[3] >> 31 ? b.w : 0.f;
+  }
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(char* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+// m[i]: all ones in the low and high half where elements 2 i and 2 i + 1 of
+// the words' group are kept, zeros where they are dropped.
+__device__ __forceinline__ void keep_masks(const uint32_t (&w)[4], uint32_t threshold,
+                                           uint32_t (&m)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void unpack8(const Row8<false>& r, float (&f)[8]) {
-  f[0] = r.a.x, f[1] = r.a.y, f[2] = r.a.z, f[3] = r.a.w;
-  f[4] = r.b.x, f[5] = r.b.y, f[6] = r.b.z, f[7] = r.b.w;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store8(void* y, int64_t row, int d, int c8, const float (&v)[8]) {
-  if (BF16) {
-    uint4 q;
-    q.x = pack_bf16x2(v[0], v[1]);
-    q.y = pack_bf16x2(v[2], v[3]);
-    q.z = pack_bf16x2(v[4], v[5]);
-    q.w = pack_bf16x2(v[6], v[7]);
-    reinterpret_cast<uint4*>(y)[row * (d / 8) + c8] = q;
-  } else {
-    float4* r = reinterpret_cast<float4*>(y) + row * (d / 4) + c8 * 2;
-    r[0] = make_float4(v[0], v[1], v[2], v[3]);
-    r[1] = make_float4(v[4], v[5], v[6], v[7]);
+    // threshold - 1 - half is negative where half >= threshold; its sign
+    // fills both bytes of the half.
+    const int lo = static_cast<int>(threshold - 1) - static_cast<int>(w[i] & 0xffffu);
+    const int hi = static_cast<int>(threshold - 1) - static_cast<int>(w[i] >> 16);
+    asm("prmt.b32 %0, %1, %2, 0xffbb;" : "=r"(m[i]) : "r"(lo), "r"(hi));
   }
 }
 
@@ -87,48 +132,66 @@ __global__ void __launch_bounds__(kCdWarps * 32)
                            int T, int d, int k, int wpt, void* y) {
   pdl_wait();
   pdl_trigger();
+  constexpr uint32_t B = Chunk<BF16>::kBytes;
   const Place at = place(wpt);
   if (at.t >= T) return;
   const int64_t t = at.t;
-  const int n8 = d / 8, lane = threadIdx.x & 31;
+  const uint32_t n8 = d / 8, lane = threadIdx.x & 31;
   uint64_t seed = 0, offset = 0;
   if (threshold) seed = rng[0], offset = rng[1];
   int row[KJ];
   float g[KJ];
+  const char* from[KJ];
   slots<KJ>(pos, gate, t, k, row, g);
-  for (int c0 = at.part * 32 * CH + lane; c0 < n8; c0 += wpt * 32 * CH) {
-    Row8<BF16> v[KJ][CH], res[CH];
+#pragma unroll
+  for (int j = 0; j < KJ; ++j) {
+    g[j] *= scale;
+    from[j] = static_cast<const char*>(o) + static_cast<int64_t>(row[j]) * n8 * B;
+  }
+  const char* rest = static_cast<const char*>(residual) + t * n8 * B;
+  char* to = static_cast<char*>(y) + t * n8 * B;
+  const PhiloxKeys keys = philox_keys(seed);
+  for (uint32_t c0 = at.part * 32 * CH + lane; c0 < n8; c0 += wpt * 32 * CH) {
+    const uint64_t at_c = static_cast<uint64_t>(c0) * B;
+    Chunk<BF16> v[KJ][CH], res[CH];
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
-      const int c8 = c0 + h * 32;
+      const bool in = c0 + h * 32 < n8;
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
-        if (row[j] >= 0 && c8 < n8)
-          v[j][h].load(o, row[j], d, c8);
+        if (row[j] >= 0 && in)
+          v[j][h].load(from[j] + at_c + h * 32 * B);
         else
           v[j][h].zero();
       }
-      if (residual && c8 < n8)
-        res[h].load(residual, t, d, c8);
+      if (residual && in)
+        res[h].load(rest + at_c + h * 32 * B);
       else
         res[h].zero();
     }
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
-      const int c8 = c0 + h * 32;
-      if (c8 >= n8) break;
+      if (c0 + h * 32 >= n8) break;
+      float acc[8] = {}, f[8];
       uint32_t w[4];
-      if (threshold) philox4x32_10(t * n8 + c8, offset, seed, w);
-      float acc[8] = {};
+      if (threshold) philox4x32_10(t * n8 + c0 + h * 32, offset, keys, w);
 #pragma unroll
-      for (int j = 0; j < KJ; ++j)
-        if (row[j] >= 0) v[j][h].fma_into(g[j], acc);  // absent slots add nothing
+      for (int j = 0; j < KJ; ++j) {
+        if (row[j] < 0) continue;  // absent slots add nothing
+        v[j][h].unpack(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(g[j], f[i], acc[i]);
+      }
       if (threshold) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = dropout_kept(w, i, threshold) ? acc[i] * scale : 0.f;
+        for (int i = 0; i < 8; ++i) acc[i] = dropout_kept(w, i, threshold) ? acc[i] : 0.f;
       }
-      if (residual) res[h].fma_into(1.f, acc);
-      store8<BF16>(y, t, d, c8, acc);
+      if (residual) {
+        res[h].unpack(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += f[i];
+      }
+      Chunk<BF16>::store(to + at_c + h * 32 * B, acc);
     }
   }
 }
@@ -167,9 +230,10 @@ __global__ void __launch_bounds__(kCdWarps * 32)
   pdl_wait();
   pdl_trigger();
   const Place at = place(wpt);
+  constexpr uint32_t B = Chunk<BF16>::kBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = at.t;
-  const int n8 = d / 8;
+  const uint32_t n8 = d / 8;
   float dot[KJ] = {};
   int row[KJ];
 #pragma unroll
@@ -179,46 +243,52 @@ __global__ void __launch_bounds__(kCdWarps * 32)
     uint64_t seed = 0, offset = 0;
     if (threshold) seed = rng[0], offset = rng[1];
     slots<KJ>(pos, gate, t, k, row, g);
+    const char* from[KJ];
 #pragma unroll
-    for (int j = 0; j < KJ; ++j) g[j] *= scale;
-    for (int c0 = at.part * 32 * CH + lane; c0 < n8; c0 += wpt * 32 * CH) {
-      Row8<BF16> v[KJ][CH], up[CH];
+    for (int j = 0; j < KJ; ++j) {
+      g[j] *= scale;
+      from[j] = static_cast<const char*>(o) + static_cast<int64_t>(row[j]) * n8 * B;
+    }
+    const char* up_row = static_cast<const char*>(dy) + t * n8 * B;
+    char* to = static_cast<char*>(d_o);
+    const PhiloxKeys keys = philox_keys(seed);
+    for (uint32_t c0 = at.part * 32 * CH + lane; c0 < n8; c0 += wpt * 32 * CH) {
+      const uint64_t at_c = static_cast<uint64_t>(c0) * B;
+      Chunk<BF16> v[KJ][CH], up[CH];
 #pragma unroll
       for (int h = 0; h < CH; ++h) {
-        const int c8 = c0 + h * 32;
-        if (c8 >= n8) break;
-        up[h].load(dy, t, d, c8);
+        if (c0 + h * 32 >= n8) break;
+        up[h].load(up_row + at_c + h * 32 * B);
 #pragma unroll
         for (int j = 0; j < KJ; ++j)
-          if (row[j] >= 0) v[j][h].load(o, row[j], d, c8);
+          if (row[j] >= 0) v[j][h].load(from[j] + at_c + h * 32 * B);
       }
 #pragma unroll
       for (int h = 0; h < CH; ++h) {
-        const int c8 = c0 + h * 32;
-        if (c8 >= n8) break;
+        if (c0 + h * 32 >= n8) break;
         // Dropped elements become zero in dy and in o (what o holds there is
-        // left out: 0 times it need not be 0), halfword masks for both.
+        // left out: 0 times it need not be 0).
         uint32_t m[4];
         if (threshold) {
-          philox4x32_10(t * n8 + c8, offset, seed, m);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m[i] = __vcmpgeu2(m[i], threshold << 16 | threshold);
+          uint32_t w[4];
+          philox4x32_10(t * n8 + c0 + h * 32, offset, keys, w);
+          keep_masks(w, threshold, m);
           up[h].mask(m);
         }
         float a[8];
-        unpack8(up[h], a);
+        up[h].unpack(a);
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
           if (row[j] < 0) continue;
           if (threshold) v[j][h].mask(m);
           float f[8];
-          unpack8(v[j][h], f);
+          v[j][h].unpack(f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             dot[j] = fmaf(a[i], f[i], dot[j]);
             f[i] = g[j] * a[i];  // g carries the scale
           }
-          store8<BF16>(d_o, row[j], d, c8, f);
+          Chunk<BF16>::store(to + (from[j] - static_cast<const char*>(o)) + at_c + h * 32 * B, f);
         }
       }
     }
@@ -240,44 +310,48 @@ __global__ void __launch_bounds__(kCdWarps * 32)
   }
 }
 
-// Warps a token: one where the tokens alone fill the GPU (eight warps on each
-// of 148 SMs), else as many as it takes, while each keeps a whole sweep of a
-// row (256 elements) to itself.
-int warps_per_token(int T, int d) {
+// Warps a token, for kernels whose warps sweep 32 CH chunks of a row at a
+// time: as many as leave each four sweeps; and where the tokens are too few
+// to fill the GPU (eight warps on each of 148 SMs), as many as leave each one.
+int warps_per_token(int T, int d, int ch) {
+  const int sweeps = (d / 8 + 32 * ch - 1) / (32 * ch);
   int wpt = 1;
-  while (wpt < kCdWarps && static_cast<int64_t>(T) * wpt < 148 * kCdWarps && wpt * 256 < d) wpt *= 2;
+  while (wpt < kCdWarps &&
+         (sweeps >= 8 * wpt ||
+          (static_cast<int64_t>(T) * wpt < 148 * kCdWarps && sweeps >= 2 * wpt)))
+    wpt *= 2;
   return wpt;
 }
 
 }  // namespace
 
 cudaError_t launch_combine_dropout(const CombineDropoutArgs& a, moe_dtype dtype, cudaStream_t s) {
-  const int wpt = warps_per_token(a.T, a.d), tokens = kCdWarps / wpt;
-  const dim3 grid((static_cast<unsigned>(a.T) + tokens - 1) / tokens);
-  auto go = [&](auto kern) {
+  auto go = [&](auto kern, int ch) {
+    const int wpt = warps_per_token(a.T, a.d, ch), tokens = kCdWarps / wpt;
+    const dim3 grid((static_cast<unsigned>(a.T) + tokens - 1) / tokens);
     return launch_kernel(kern, grid, dim3(kCdWarps * 32), 0, s, 1, true, a.o, a.pos, a.gate,
                          a.residual, a.rng, a.threshold, a.scale, a.T, a.d, a.k, wpt, a.y);
   };
   if (dtype == MOE_BF16)
-    return a.k <= 2 ? go(combine_dropout_kernel<true, 2, 4>)
-                    : go(combine_dropout_kernel<true, kMaxK, 2>);
-  return a.k <= 2 ? go(combine_dropout_kernel<false, 2, 2>)
-                  : go(combine_dropout_kernel<false, kMaxK, 1>);
+    return a.k <= 2 ? go(combine_dropout_kernel<true, 2, 2>, 2)
+                    : go(combine_dropout_kernel<true, kMaxK, 1>, 1);
+  return a.k <= 2 ? go(combine_dropout_kernel<false, 2, 1>, 1)
+                  : go(combine_dropout_kernel<false, kMaxK, 1>, 1);
 }
 
 cudaError_t launch_combine_dropout_backward(const CombineDropoutArgs& a, moe_dtype dtype,
                                             cudaStream_t s) {
-  const int wpt = warps_per_token(a.T, a.d), tokens = kCdWarps / wpt;
-  const dim3 grid((static_cast<unsigned>(a.T) + tokens - 1) / tokens);
-  auto go = [&](auto kern) {
+  auto go = [&](auto kern, int ch) {
+    const int wpt = warps_per_token(a.T, a.d, ch), tokens = kCdWarps / wpt;
+    const dim3 grid((static_cast<unsigned>(a.T) + tokens - 1) / tokens);
     return launch_kernel(kern, grid, dim3(kCdWarps * 32), 0, s, 1, true, a.dy, a.o, a.pos, a.gate,
                          a.rng, a.threshold, a.scale, a.T, a.d, a.k, wpt, a.d_o, a.dgate);
   };
   if (dtype == MOE_BF16)
-    return a.k <= 2 ? go(combine_dropout_backward_kernel<true, 2, 2>)
-                    : go(combine_dropout_backward_kernel<true, kMaxK, 1>);
-  return a.k <= 2 ? go(combine_dropout_backward_kernel<false, 2, 1>)
-                  : go(combine_dropout_backward_kernel<false, kMaxK, 1>);
+    return a.k <= 2 ? go(combine_dropout_backward_kernel<true, 2, 2>, 2)
+                    : go(combine_dropout_backward_kernel<true, kMaxK, 1>, 1);
+  return a.k <= 2 ? go(combine_dropout_backward_kernel<false, 2, 1>, 1)
+                  : go(combine_dropout_backward_kernel<false, kMaxK, 1>, 1);
 }
 
 }  // namespace moe

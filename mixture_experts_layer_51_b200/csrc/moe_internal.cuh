@@ -378,11 +378,6 @@ struct Row8<true> {
     v = __ldcs(reinterpret_cast<const uint4*>(o) + row * (d / 8) + c8);
   }
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
-  // Elements 2 i and 2 i + 1 stay where the low and high half of m[i] are all
-  // ones, and become zero where they are zeros.
-  __device__ __forceinline__ void mask(const uint32_t (&m)[4]) {
-    v.x &= m[0], v.y &= m[1], v.z &= m[2], v.w &= m[3];
-  }
   // acc[i] += g * element i (bf16 -> fp32 is exact: the high 16 bits).
   __device__ __forceinline__ void fma_into(float g, float (&acc)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -402,16 +397,6 @@ struct Row8<false> {
     b = __ldcs(r + 1);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void mask(const uint32_t (&m)[4]) {
-    a.x = m[0] & 1u ? a.x : 0.f;
-    a.y = m[0] >> 31 ? a.y : 0.f;
-    a.z = m[1] & 1u ? a.z : 0.f;
-    a.w = m[1] >> 31 ? a.w : 0.f;
-    b.x = m[2] & 1u ? b.x : 0.f;
-    b.y = m[2] >> 31 ? b.y : 0.f;
-    b.z = m[3] & 1u ? b.z : 0.f;
-    b.w = m[3] >> 31 ? b.w : 0.f;
-  }
   __device__ __forceinline__ void fma_into(float g, float (&acc)[8]) const {
     acc[0] = fmaf(g, a.x, acc[0]);
     acc[1] = fmaf(g, a.y, acc[1]);

@@ -18,20 +18,31 @@ __host__ __device__ __forceinline__ void philox_round(uint32_t (&c)[4], uint32_t
   c[3] = static_cast<uint32_t>(a);
 }
 
-// The four words of counter (n, offset) under key `seed`.
-__host__ __device__ __forceinline__ void philox4x32_10(uint64_t n, uint64_t offset, uint64_t seed,
-                                                       uint32_t (&c)[4]) {
+// The keys of the ten rounds, for callers that make many counters' words.
+struct PhiloxKeys {
+  uint32_t k[20];
+};
+__host__ __device__ __forceinline__ PhiloxKeys philox_keys(uint64_t seed) {
+  PhiloxKeys keys;
+  keys.k[0] = static_cast<uint32_t>(seed);
+  keys.k[1] = static_cast<uint32_t>(seed >> 32);
+#pragma unroll
+  for (int r = 1; r < 10; ++r) {
+    keys.k[2 * r] = keys.k[2 * r - 2] + 0x9E3779B9u;
+    keys.k[2 * r + 1] = keys.k[2 * r - 1] + 0xBB67AE85u;
+  }
+  return keys;
+}
+
+// The four words of counter (n, offset).
+__host__ __device__ __forceinline__ void philox4x32_10(uint64_t n, uint64_t offset,
+                                                       const PhiloxKeys& keys, uint32_t (&c)[4]) {
   c[0] = static_cast<uint32_t>(n);
   c[1] = static_cast<uint32_t>(n >> 32);
   c[2] = static_cast<uint32_t>(offset);
   c[3] = static_cast<uint32_t>(offset >> 32);
-  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
 #pragma unroll
-  for (int r = 0; r < 10; ++r) {
-    philox_round(c, k0, k1);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
-  }
+  for (int r = 0; r < 10; ++r) philox_round(c, keys.k[2 * r], keys.k[2 * r + 1]);
 }
 
 // Dropout's decision for eight consecutive elements (element group n) from the
@@ -49,7 +60,7 @@ __host__ __device__ __forceinline__ bool dropout_kept(const uint32_t (&w)[4], in
 __host__ __device__ __forceinline__ uint32_t dropout_keep8(uint64_t n, uint64_t offset,
                                                            uint64_t seed, uint32_t threshold) {
   uint32_t w[4];
-  philox4x32_10(n, offset, seed, w);
+  philox4x32_10(n, offset, philox_keys(seed), w);
   uint32_t keep = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) keep |= (dropout_kept(w, i, threshold) ? 1u : 0u) << i;

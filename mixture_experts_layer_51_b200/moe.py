@@ -708,24 +708,27 @@ class MoELayer:
 
 
 # ---------------------------------------------------------------- training
-_MASK_TYPES = (torch.bool, torch.uint8)
-
-
-def _tensor(t, name, dtypes, shape, dev):
+def _tensor(t, name, dtype, shape, dev):
     """The address of an argument that the kernels will read or write: its
     type, shape, device and dense layout are checked here, because a raw
     pointer carries none of them.  None passes as NULL."""
     if t is None:
         return None
-    if t.dtype is not dtypes and t.dtype not in (dtypes if type(dtypes) is tuple else (dtypes,)):
-        raise TypeError(f"{name} is {t.dtype}, expected {dtypes}")
-    if tuple(t.shape) != shape:
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} is not contiguous")
+
+
+def _mask(mask, T, dev):
+    """A bool or uint8 mask's address (a torch bool is one byte, 0 or 1)."""
+    kind = torch.uint8 if mask is not None and mask.dtype is torch.uint8 else torch.bool
+    return _tensor(mask, "mask", kind, (T,), dev)
 
 
 def _cuda_device(t, name):
@@ -734,15 +737,22 @@ def _cuda_device(t, name):
     return t.device
 
 
+# The current stream's handle: torch.cuda.current_stream builds a Stream object
+# around it, which takes as long as a kernel launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(fn, where, dev, stream, *args):
     """fn(*args, stream) with ``dev`` current (its own stream if none is given)."""
-    s = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    s = stream.cuda_stream if stream is not None else _raw_stream(dev.index)
     if torch.cuda.current_device() == dev.index:
         status = fn(*args, s)
     else:
         with torch.cuda.device(dev):
             status = fn(*args, s)
-    _check(status, where)
+    if status != MOE_OK:
+        raise MoeError(status, where)
 
 
 def _empty(shape, dtype, dev, stream):
@@ -786,7 +796,7 @@ def moe_balance_loss(scores, idx, coef, mask=None, loss=None, prob_sum=None, cou
                     stream)
     _launch(lib().moe_balance_loss, "moe_balance_loss", dev, stream,
             _tensor(scores, "scores", f32, (E, T), dev), _tensor(idx, "idx", i32, (T, k), dev),
-            _tensor(mask, "mask", _MASK_TYPES, (T,), dev), T, E, k, coef,
+            _mask(mask, T, dev), T, E, k, coef,
             _tensor(loss, "loss", f32, (1,), dev), _tensor(prob_sum, "prob_sum", f32, (E,), dev),
             _tensor(counts, "counts", i32, (E,), dev), _tensor(tokens, "tokens", i32, (1,), dev),
             ws.data_ptr(), ws.numel() * ws.element_size())
@@ -816,10 +826,18 @@ def moe_route_backward(x, Wg, idx, gate=None, dgate=None, scores=None, counts=No
     i32, f32, dt = torch.int32, torch.float32, x.dtype
     code = _dtype_code(x)
     out = {}
-    for name, given, shape, dtype in (("dx", dx, (T, d), dt), ("dWg", dWg, (d, E), f32),
-                                      ("dbias", dbias, (E,), f32)):
-        if name in outputs:
-            out[name] = given if given is not None else _empty(shape, dtype, dev, stream)
+    if "dx" in outputs:
+        out["dx"] = dx = dx if dx is not None else _empty((T, d), dt, dev, stream)
+    else:
+        dx = None
+    if "dWg" in outputs:
+        out["dWg"] = dWg = dWg if dWg is not None else _empty((d, E), f32, dev, stream)
+    else:
+        dWg = None
+    if "dbias" in outputs:
+        out["dbias"] = dbias = dbias if dbias is not None else _empty(E, f32, dev, stream)
+    else:
+        dbias = None
     if len(out) != len(outputs):
         raise ValueError(f"outputs {outputs}: dx, dWg and dbias, each at most once")
     ws = _workspace(ws, 0 if ws is not None else
@@ -831,11 +849,10 @@ def moe_route_backward(x, Wg, idx, gate=None, dgate=None, scores=None, counts=No
             _tensor(gate, "gate", f32, (T, k), dev), _tensor(dgate, "dgate", f32, (T, k), dev),
             _tensor(counts, "counts", i32, (E,), dev), _tensor(tokens, "tokens", i32, (1,), dev),
             _tensor(dloss, "dloss", f32, (1,), dev), coef,
-            _tensor(mask, "mask", _MASK_TYPES, (T,), dev),
+            _mask(mask, T, dev),
             _tensor(dx_acc, "dx_acc", dt, (T, d), dev), T, d, E, k, code, ctypes.byref(opt),
-            _tensor(out.get("dx"), "dx", dt, (T, d), dev),
-            _tensor(out.get("dWg"), "dWg", f32, (d, E), dev),
-            _tensor(out.get("dbias"), "dbias", f32, (E,), dev), ws.data_ptr(),
+            _tensor(dx, "dx", dt, (T, d), dev), _tensor(dWg, "dWg", f32, (d, E), dev),
+            _tensor(dbias, "dbias", f32, (E,), dev), ws.data_ptr(),
             ws.numel() * ws.element_size())
     return out
 
