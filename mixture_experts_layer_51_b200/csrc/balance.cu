@@ -8,11 +8,17 @@
 // floating-point atomics: the sums do not depend on scheduling).
 //
 // Bound by reading the scores once, and for small batches by launches and
-// round trips to memory.  So there are two forms.  A batch of up to 1 MB is
-// one launch: a cluster of eight CTAs whose first adds the others' sums out
-// of their shared memory.  A larger one takes a CTA on every SM, and a second
-// launch adds the slices from the workspace.
-// MEASURED
+// round trips to memory.  So a batch of up to 64 KB (scores and indices) is
+// one CTA's, one of up to 512 KB a cluster's of eight CTAs, whose first adds
+// the others' sums out of their shared memory, and a larger one takes a CTA on
+// every SM and a second launch that adds the slices from the workspace.
+//
+// Measured back to back in a graph on one B200: 256 tokens of 4 experts 3.6 us
+// (4.4 as a cluster), 80 KB 4.6 us as a cluster (6.9 in one CTA), 295 KB 5.5
+// (6.1 in two launches), 1.2 MB 6.2 in two launches (7.7 as a cluster),
+// 100003 tokens of 64 experts with a mask (29 MB) 13.1 us; reading that takes
+// 4.4 us at 6.56 TB/s, the rest is two launches, two rounds of loads and the
+// last sums.
 
 #include "moe_internal.cuh"
 
@@ -22,10 +28,11 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
-constexpr int64_t kClusterBytes = 1 << 20;
+constexpr int64_t kOneBytes = 1 << 16;      // scores and indices that one CTA takes,
+constexpr int64_t kClusterBytes = 1 << 19;  // and one cluster
 constexpr int kMaxSlices = 148;     // one CTA on each SM
 constexpr int kMinSlice = 256;      // tokens
-constexpr int kBatch = 8;           // scores a lane has on their way per expert
+constexpr int kBatch = 12;          // scores a lane has on their way per expert
 
 // A slice's sums: S_e, counts_e, N.
 struct Partial {
@@ -38,9 +45,6 @@ struct Partial {
 struct Slices {
   int n, len;  // slices, tokens in each (a multiple of 32; the last may hold fewer)
 };
-bool one_cluster(int T, int E, int k) {
-  return static_cast<int64_t>(T) * (E + k) * 4 <= kClusterBytes;
-}
 Slices slices(int T) {
   const int64_t per = (static_cast<int64_t>(T) + kMaxSlices - 1) / kMaxSlices;
   const int64_t len = per < kMinSlice ? kMinSlice : (per + 31) / 32 * 32;
@@ -48,7 +52,7 @@ Slices slices(int T) {
 }
 
 // The sums over tokens t0 .. t1 - 1 into `out` (shared memory), by the whole
-// CTA.  A warp takes an expert's scores, 256 tokens at a time; with fewer
+// CTA.  A warp takes an expert's scores, 32 kBatch tokens at a time; with fewer
 // than 32 experts several warps share one, each with a part of the tokens.
 __device__ void sum_slice(const float* __restrict__ scores, const int32_t* __restrict__ idx,
                           const uint8_t* __restrict__ mask, int T, int E, int k, uint32_t t0,
@@ -62,6 +66,18 @@ __device__ void sum_slice(const float* __restrict__ scores, const int32_t* __res
   // Experts of a round of warps (a power of two), and warps to an expert.
   const int wide = E > 16 ? 32 : E > 8 ? 16 : E > 4 ? 8 : E > 2 ? 4 : E;
   const int share = kWarps / wide, e0 = warp % wide, q = warp / wide;
+  // The first tokens' experts are asked for before the scores, and counted
+  // after them.
+  auto load = [&](uint32_t t, int (&sel)[kMaxK]) {
+    const bool counted = t < t1 && (!mask || mask[t]);
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      sel[j] = t < t1 && j < k ? __ldg(idx + static_cast<int64_t>(t) * k + j) : -1;
+    return counted;
+  };
+  int sel[kMaxK];
+  uint32_t tok = t0 + tid;
+  bool counted = load(tok, sel);
   float s[2] = {0.f, 0.f};
   for (uint32_t t = t0 + q * 32 * kBatch + lane; t < t1; t += share * 32 * kBatch) {
     float v[2][kBatch];
@@ -84,17 +100,15 @@ __device__ void sum_slice(const float* __restrict__ scores, const int32_t* __res
       for (int h = 0; h < 2; ++h) s[h] += on >> i & 1u ? v[h][i] : 0.f;
   }
   __syncthreads();  // the counters are zero
-  for (uint32_t t = t0 + tid; t - lane < t1; t += kThreads) {
-    const bool counted = t < t1 && (!mask || mask[t]);
+  for (;;) {
     const unsigned any = __ballot_sync(0xffffffffu, counted);
     if (lane == 0 && any) atomicAdd(&tokens_s, __popc(any));
-    int sel[kMaxK];
 #pragma unroll
     for (int j = 0; j < kMaxK; ++j)
-      sel[j] = counted && j < k ? __ldg(idx + static_cast<int64_t>(t) * k + j) : -1;
-#pragma unroll
-    for (int j = 0; j < kMaxK; ++j)
-      if (sel[j] >= 0 && sel[j] < E) atomicAdd(&count_s[sel[j]], 1);
+      if (counted && sel[j] >= 0 && sel[j] < E) atomicAdd(&count_s[sel[j]], 1);
+    tok += kThreads;
+    if (tok - lane >= t1) break;
+    counted = load(tok, sel);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -133,35 +147,40 @@ __device__ __forceinline__ void finish(int e, int E, int k, float coef, float su
   }
 }
 
+// C CTAs of one cluster.
+template <int C>
 __global__ void __launch_bounds__(kThreads, 1) balance_cluster_kernel(const BalanceArgs a, int len) {
   __shared__ Partial mine;
   const int tid = threadIdx.x;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = C > 1 ? cluster_ctarank() : 0;
   pdl_wait();
   pdl_trigger();
   const int t0 = min(a.T, static_cast<int>(rank) * len), t1 = min(a.T, t0 + len);
   sum_slice(a.scores, a.idx, a.mask, a.T, a.E, a.k, t0, t1, mine);
-  cluster_sync();
+  if (C > 1)
+    cluster_sync();
+  else
+    __syncthreads();
   if (rank == 0 && tid < kMaxE) {
     float sum = 0.f;
     int32_t count = 0, tokens = 0;
-    uint32_t v[kCluster][3];
+    uint32_t v[C][3];
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) {
+    for (int r = 0; r < C; ++r) {
       const uint32_t from = mapa_shared(smem_u32(&mine), r);
       v[r][0] = ld_shared_cluster_u32(from + offsetof(Partial, sum) + 4 * tid);
       v[r][1] = ld_shared_cluster_u32(from + offsetof(Partial, count) + 4 * tid);
       v[r][2] = ld_shared_cluster_u32(from + offsetof(Partial, tokens));
     }
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) {
+    for (int r = 0; r < C; ++r) {
       sum += __uint_as_float(v[r][0]);
       count += static_cast<int32_t>(v[r][1]);
       tokens += static_cast<int32_t>(v[r][2]);
     }
     finish(tid, a.E, a.k, a.coef, sum, count, tokens, a);
   }
-  cluster_sync();  // the others' shared memory lives until it has been read
+  if (C > 1) cluster_sync();  // the others' shared memory lives until it has been read
 }
 
 __global__ void __launch_bounds__(kThreads, 1) balance_slice_kernel(const BalanceArgs a, int len) {
@@ -211,11 +230,12 @@ __global__ void __launch_bounds__(kThreads, 1) balance_finish_kernel(const Balan
 size_t balance_scratch_bytes(int T) { return sizeof(Partial) * (slices(T).n + 1); }
 
 cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
-  if (one_cluster(a.T, a.E, a.k)) {
-    const int len = (a.T + 32 * kCluster - 1) / (32 * kCluster) * 32;
-    return launch_kernel(balance_cluster_kernel, dim3(kCluster), dim3(kThreads), 0, s, kCluster,
-                         true, a, len);
-  }
+  const int64_t bytes = static_cast<int64_t>(a.T) * (a.E + a.k) * 4;
+  if (bytes <= kOneBytes)
+    return launch_kernel(balance_cluster_kernel<1>, dim3(1), dim3(kThreads), 0, s, 1, true, a, a.T);
+  if (bytes <= kClusterBytes)
+    return launch_kernel(balance_cluster_kernel<kCluster>, dim3(kCluster), dim3(kThreads), 0, s,
+                         kCluster, true, a, (a.T + 32 * kCluster - 1) / (32 * kCluster) * 32);
   const Slices sl = slices(a.T);
   const cudaError_t err = launch_kernel(balance_slice_kernel, dim3(sl.n), dim3(kThreads), 0, s, 1,
                                         true, a, sl.len);
