@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kDzThreads = 4 * kRbTokens;
 constexpr int kCols = 64;          // fp32 products: columns of one CTA,
-constexpr int kTile = 32;          // tokens of one tile
+constexpr int kTile = 64;          // tokens of one tile
 constexpr int kThreads = 256;
 
 // Token ranges for `cols` column blocks: the number that needs the fewest
@@ -52,7 +52,7 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   const int cols = tc ? kRbTcCols : kCols, tile = tc ? kRbTcTokens : kTile;
   p.cols = (d + cols - 1) / cols;
   p.tiles = (T + tile - 1) / tile;
-  p.ranges = T > 0 ? pick_ranges(p.cols, p.tiles, tc ? 1 : 4) : 0;
+  p.ranges = T > 0 ? pick_ranges(p.cols, p.tiles, tc ? 1 : 2) : 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -200,80 +200,168 @@ __global__ void __launch_bounds__(kDzThreads)
         (part[0][0][tok] + part[0][1][tok]) + (part[0][2][tok] + part[0][3][tok]);
 }
 
-// Both products of an fp32 layer, on fp32 FMA: thread (column, quarter) keeps
-// its column's share of dW_g (a quarter of the experts) and its column of W_g
-// in registers, and makes dx for a quarter of the tile's tokens.
+// Both products of an fp32 layer, on fp32 FMA.  A CTA owns 64 columns and a
+// range of tokens, in tiles of 64 tokens that cp.async brings two stages deep.
+// Register tiles of 4 x 4 in both products (columns x experts over the tokens;
+// tokens x columns over the experts) take two 16-byte shared-memory reads for
+// 16 FMA.  With fewer than 64 experts the threads that dW_g does not need
+// share out the tile's tokens, and are added up when the range is done.
 template <int EP>
-__global__ void __launch_bounds__(kThreads)
+struct SimtSmem {
+  float x[2][kTile][kCols];
+  float dz[2][kTile][EP];
+  float w[EP][kCols];        // W_g of the columns, expert-major
+  float4 scratch[kThreads];
+  uint32_t last;
+};
+
+template <int EP>
+__global__ void __launch_bounds__(kThreads, 2)
     route_products_kernel(const RouteBackwardArgs a, const RouteSums sums, int ranges, int tiles,
                           const float* __restrict__ dz) {
-  constexpr int QE = EP / 4;
-  __shared__ __align__(16) float dz_s[kTile][EP];
-  __shared__ float x_s[kTile][kCols];
+  constexpr int EG = EP / 4;                 // expert groups of dW_g
+  constexpr int TG = kThreads / (16 * EG);   // token groups of dW_g
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SimtSmem<EP>& sm = *reinterpret_cast<SimtSmem<EP>*>(smem_raw);
   const float* x = static_cast<const float*>(a.x);
   const float* Wg = static_cast<const float*>(a.Wg);
   const float* dx_acc = static_cast<const float*>(a.dx_acc);
   float* dx = static_cast<float*>(a.dx);
-  const int tid = threadIdx.x, col = tid % kCols, q = tid / kCols;
-  const int c = blockIdx.x * kCols + col;
-  const bool in = c < a.d;
-  pdl_wait();
-  pdl_trigger();
-  float w[EP], acc[QE];
-#pragma unroll
-  for (int e = 0; e < EP; ++e)
-    w[e] = dx && in && e < a.E ? Wg[static_cast<int64_t>(c) * a.E + e] : 0.f;
-#pragma unroll
-  for (int e = 0; e < QE; ++e) acc[e] = 0.f;
+  const int tid = threadIdx.x, cg = tid % 16, c0 = blockIdx.x * kCols;
+  const int cols = min(kCols, a.d - c0);
+  const bool in = 4 * cg < cols;             // columns come in eights
+  const int64_t col = c0 + 4 * cg;
   const int t0 = static_cast<int>(static_cast<int64_t>(blockIdx.y) * tiles / ranges) * kTile;
   const int t1 = min(a.T, static_cast<int>(static_cast<int64_t>(blockIdx.y + 1) * tiles / ranges) *
                               kTile);
-  for (int tb = t0; tb < t1; tb += kTile) {
-    __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  auto load = [&](int tb, int st) {
     const int rows = min(kTile, t1 - tb);
-    for (int i = tid; i < kTile * EP; i += kThreads)
-      (&dz_s[0][0])[i] = i < rows * EP ? dz[static_cast<int64_t>(tb) * EP + i] : 0.f;
     if (a.dWg)
-      for (int r = q; r < kTile; r += 4) {
-        const int t = tb + r;
-        const bool use = in && r < rows && (!a.mask || a.mask[t]);
-        x_s[r][col] = use ? x[static_cast<int64_t>(t) * a.d + c] : 0.f;
+#pragma unroll
+      for (int r = tid / 16; r < kTile; r += kThreads / 16) {
+        // Nothing is read of a padding token (nor past the range): zeros.
+        const bool use = in && r < rows && (!a.mask || a.mask[tb + r]);
+        cp_async16(smem_u32(&sm.x[st][r][4 * cg]),
+                   use ? x + static_cast<int64_t>(tb + r) * a.d + col : x, use ? 16 : 0);
       }
+    const float* from = dz + static_cast<int64_t>(tb) * EP;
+#pragma unroll
+    for (int i = tid; i < kTile * EP / 4; i += kThreads) {
+      const bool use = i < rows * EP / 4;
+      cp_async16(smem_u32(&sm.dz[st][0][0] + 4 * i), use ? from + 4 * i : from, use ? 16 : 0);
+    }
+    cp_async_commit();
+  };
+  if (t0 < t1) load(t0, 0);
+  if (dx) {
+    for (int i = tid; i < EP * kCols; i += kThreads) (&sm.w[0][0])[i] = 0.f;
     __syncthreads();
-    if (a.dWg)
-      for (int r = 0; r < kTile; ++r) {
-        const float xv = x_s[r][col];
+    int c = tid / a.E, e = tid % a.E;
+    const int dc = kThreads / a.E, de = kThreads % a.E;
+    for (int i = tid; i < cols * a.E; i += kThreads) {
+      sm.w[e][c] = Wg[static_cast<int64_t>(c0) * a.E + i];
+      c += dc;
+      e += de;
+      if (e >= a.E) e -= a.E, ++c;
+    }
+  }
+  const int eg = tid / 16 % EG, tg = tid / (16 * EG);
+  float acc[4][4] = {};
+  int st = 0;
+  for (int tb = t0; tb < t1; tb += kTile, st ^= 1) {
+    const int rows = min(kTile, t1 - tb);
+    if (tb + kTile < t1)
+      load(tb + kTile, st ^ 1);
+    else
+      cp_async_commit();  // one group a tile, so that the wait counts tiles
+    // This thread's four tokens and columns of dx.
+    const int row = tid / 16 * 4;
+    float4 v[4];
 #pragma unroll
-        for (int e = 0; e < QE; ++e) acc[e] = fmaf(xv, dz_s[r][q * QE + e], acc[e]);
-      }
-    if (dx && in)
-      for (int r = q; r < rows; r += 4) {
-        const int64_t at = static_cast<int64_t>(tb + r) * a.d + c;
-        float v = 0.f;
+    for (int i = 0; i < 4; ++i)
+      v[i] = dx_acc && dx && in && row + i < rows
+                 ? *reinterpret_cast<const float4*>(
+                       dx_acc + static_cast<int64_t>(tb + row + i) * a.d + col)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    cp_async_wait<1>();
+    __syncthreads();
+    if (a.dWg) {
+#pragma unroll 4
+      for (int r = tg; r < kTile; r += TG) {
+        const float4 xv = *reinterpret_cast<const float4*>(&sm.x[st][r][4 * cg]);
+        const float4 zv = *reinterpret_cast<const float4*>(&sm.dz[st][r][4 * eg]);
+        const float xs[4] = {xv.x, xv.y, xv.z, xv.w}, zs[4] = {zv.x, zv.y, zv.z, zv.w};
 #pragma unroll
-        for (int e = 0; e < EP; ++e) v = fmaf(dz_s[r][e], w[e], v);
-        dx[at] = dx_acc ? v + dx_acc[at] : v;
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(xs[i], zs[e], acc[i][e]);
       }
+    }
+    if (dx) {
+      float o[4][4] = {};
+#pragma unroll 2
+      for (int e = 0; e < EP; e += 4) {
+        float zs[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 zv = *reinterpret_cast<const float4*>(&sm.dz[st][row + i][e]);
+          zs[i][0] = zv.x, zs[i][1] = zv.y, zs[i][2] = zv.z, zs[i][3] = zv.w;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 wv = *reinterpret_cast<const float4*>(&sm.w[e + u][4 * cg]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[i][0] = fmaf(zs[i][u], wv.x, o[i][0]);
+            o[i][1] = fmaf(zs[i][u], wv.y, o[i][1]);
+            o[i][2] = fmaf(zs[i][u], wv.z, o[i][2]);
+            o[i][3] = fmaf(zs[i][u], wv.w, o[i][3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (in && row + i < rows)
+          *reinterpret_cast<float4*>(dx + static_cast<int64_t>(tb + row + i) * a.d + col) =
+              make_float4(v[i].x + o[i][0], v[i].y + o[i][1], v[i].z + o[i][2], v[i].w + o[i][3]);
+    }
+    __syncthreads();  // the next load goes to this stage
   }
   if (sums.dbias && tid < 32)
     for (int e = blockIdx.x + blockIdx.y * gridDim.x; e < a.E; e += gridDim.x * gridDim.y)
       sum_bias(sums, e, tid);
   if (!a.dWg) return;
-  if (in)
+  // The token groups' parts, in order, then the range's part to memory.
+  float* part = &sm.x[0][0][0];  // [TG][64 columns][EP]: 16 KB
 #pragma unroll
-    for (int e = 0; e < QE; ++e)
-      if (q * QE + e < a.E)
-        sums.dw[(static_cast<int64_t>(blockIdx.y) * a.d + c) * a.E + q * QE + e] = acc[e];
-  __shared__ uint32_t last;
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[(tg * kCols + 4 * cg + i) * EP + 4 * eg + e] = acc[i][e];
+  __syncthreads();
+  {
+    float* out = sums.dw + (static_cast<int64_t>(blockIdx.y) * a.d + c0) * a.E;
+    int c = tid / a.E, e = tid % a.E;
+    const int dc = kThreads / a.E, de = kThreads % a.E;
+    for (int i = tid; i < cols * a.E; i += kThreads) {
+      float sum = part[c * EP + e];
+#pragma unroll
+      for (int g = 1; g < TG; ++g) sum += part[(g * kCols + c) * EP + e];
+      out[i] = sum;
+      c += dc;
+      e += de;
+      if (e >= a.E) e -= a.E, ++c;
+    }
+  }
   __threadfence();
   __syncthreads();
   if (tid == 0)
-    last = atomicAdd(sums.tickets + blockIdx.x, 1u) + 1 == static_cast<uint32_t>(ranges);
+    sm.last = atomicAdd(sums.tickets + blockIdx.x, 1u) + 1 == static_cast<uint32_t>(ranges);
   __syncthreads();
-  if (!last) return;
+  if (!sm.last) return;
   __threadfence();
-  sum_ranges(sums, blockIdx.x * kCols, min(kCols, a.d - static_cast<int>(blockIdx.x) * kCols), tid,
-             kThreads);
+  sum_ranges(sums, c0, cols, tid, kThreads, sm.scratch, [] { __syncthreads(); });
 }
 
 // The bias alone: one warp an expert.
@@ -285,15 +373,18 @@ __global__ void __launch_bounds__(32) route_bias_kernel(const RouteSums sums) {
 
 cudaError_t launch_products(const RouteBackwardArgs& a, const RouteBackwardPlan& p,
                             const RouteSums& sums, const float* dz, cudaStream_t s) {
-  auto go = [&](auto kern) {
-    return launch_kernel(kern, dim3(p.cols, p.ranges), dim3(kThreads), 0, s, 1, true, a, sums,
+  auto go = [&](auto kern, size_t smem) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3(p.cols, p.ranges), dim3(kThreads), smem, s, 1, true, a, sums,
                          p.ranges, p.tiles, dz);
   };
   switch (p.EP) {
-    case 8: return go(route_products_kernel<8>);
-    case 16: return go(route_products_kernel<16>);
-    case 32: return go(route_products_kernel<32>);
-    default: return go(route_products_kernel<64>);
+    case 8: return go(route_products_kernel<8>, sizeof(SimtSmem<8>));
+    case 16: return go(route_products_kernel<16>, sizeof(SimtSmem<16>));
+    case 32: return go(route_products_kernel<32>, sizeof(SimtSmem<32>));
+    default: return go(route_products_kernel<64>, sizeof(SimtSmem<64>));
   }
 }
 

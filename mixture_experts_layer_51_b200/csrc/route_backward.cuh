@@ -57,37 +57,51 @@ __device__ __forceinline__ void sum_bias(const RouteSums& s, int e, int lane) {
 }
 
 // dW_g of columns c0 .. c0 + cols - 1: the ranges' parts in order, by `n`
-// threads (this one is `i`).  After a time-out in the products nothing here
-// is right: NaN says so.
-__device__ __forceinline__ void sum_ranges(const RouteSums& s, int c0, int cols, int i, int n) {
-  const int64_t plane = static_cast<int64_t>(s.d) * s.E;
-  const int64_t at = static_cast<int64_t>(c0) * s.E;
+// threads (this one is `i`; sync() is a barrier for all of them, scratch holds
+// n pieces of 16 bytes).  One thread block reads what a whole column block
+// wrote, so what counts is how many loads are on their way: eight pieces a
+// thread, or, with fewer pieces than threads, several threads to a piece.
+// After a time-out in the products nothing here is right: NaN says so.
+template <typename Sync>
+__device__ __forceinline__ void sum_ranges(const RouteSums& s, int c0, int cols, int i, int n,
+                                           float4* scratch, Sync sync) {
+  const int64_t plane = static_cast<int64_t>(s.d) * s.E / 4, at = static_cast<int64_t>(c0) * s.E;
   const bool failed = *static_cast<volatile int32_t*>(s.err) != 0;
   const int count = cols * s.E / 4;  // columns come in eights
   const float4* from = reinterpret_cast<const float4*>(s.dw + at);
   float4* to = reinterpret_cast<float4*>(s.dWg + at);
-  // Eight pieces at a time: one thread block reads what a whole column block
-  // wrote, so what counts is how many loads are on their way.
+  auto add = [](float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; };
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float nan = __int_as_float(0x7fc00000);
+  if (2 * count <= n) {
+    const int groups = n / count, v = i % count, g = i / count;
+    float4 sum = zero;
+    if (g < groups) {
+#pragma unroll 8
+      for (int r = g; r < s.ranges; r += groups) add(sum, __ldcg(from + r * plane + v));
+    }
+    scratch[i] = sum;
+    sync();
+    if (i < count) {
+      for (int q = 1; q < groups; ++q) add(sum, scratch[q * count + i]);
+      to[i] = failed ? make_float4(nan, nan, nan, nan) : sum;
+    }
+    return;
+  }
   constexpr int P = 8;
   for (int v0 = i; v0 < count; v0 += P * n) {
     float4 sum[P];
 #pragma unroll
-    for (int j = 0; j < P; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < P; ++j) sum[j] = zero;
 #pragma unroll 2
     for (int r = 0; r < s.ranges; ++r) {
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        if (v0 + j * n >= count) continue;
-        const float4 part = __ldcg(from + r * (plane / 4) + v0 + j * n);
-        sum[j].x += part.x, sum[j].y += part.y, sum[j].z += part.z, sum[j].w += part.w;
-      }
+      for (int j = 0; j < P; ++j)
+        if (v0 + j * n < count) add(sum[j], __ldcg(from + r * plane + v0 + j * n));
     }
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      if (v0 + j * n >= count) continue;
-      if (failed) sum[j].x = sum[j].y = sum[j].z = sum[j].w = __int_as_float(0x7fc00000);
-      to[v0 + j * n] = sum[j];
-    }
+    for (int j = 0; j < P; ++j)
+      if (v0 + j * n < count) to[v0 + j * n] = failed ? make_float4(nan, nan, nan, nan) : sum[j];
   }
 }
 

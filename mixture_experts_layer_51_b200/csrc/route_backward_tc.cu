@@ -474,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       epilogue_sync();
       if (c.last) {
         __threadfence();
-        sum_ranges(p.sums, c0, min(kRbTcCols, p.d - c0), et, kEpilogue);
+        sum_ranges(p.sums, c0, min(kRbTcCols, p.d - c0), et, kEpilogue,
+                   reinterpret_cast<float4*>(smem), epilogue_sync);
       }
     }
   }
