@@ -64,7 +64,9 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   const size_t row = tc ? 128 * dz_terms(E).blocks : sizeof(float) * p.EP;
   p.dz = take(row * T);
   p.bias = take(sizeof(float) * kMaxE * p.blocks);
-  p.dw = take(sizeof(float) * d * E * p.ranges);
+  p.dw = take(tc && dz_terms(E).blocks == 3
+                  ? static_cast<size_t>(kRbPartBytes) * p.cols * p.ranges
+                  : sizeof(float) * d * E * p.ranges);
   p.total = at;
   return p;
 }
@@ -76,8 +78,9 @@ __device__ __forceinline__ float bf16_round(float v) {
 // dz of 64 tokens, four threads a token (each a quarter of the experts, kept
 // in registers so that the scores are read once), and its column sums.  TC:
 // dz leaves as bf16 terms, else as fp32 rows of EP; either way by way of
-// shared memory, in whole 16-byte pieces of contiguous rows.
-template <bool TC>
+// shared memory, in whole 16-byte pieces of contiguous rows.  Q: experts a
+// thread has room for (a quarter of E, rounded up to a power of two).
+template <bool TC, int Q>
 __global__ void __launch_bounds__(kDzThreads)
     route_dz_kernel(const RouteBackwardArgs a, int EP, DzTerms terms, void* __restrict__ dz,
                     float* __restrict__ bias_part, int32_t* __restrict__ err,
@@ -104,12 +107,14 @@ __global__ void __launch_bounds__(kDzThreads)
   const float dloss = a.counts && a.dloss ? *a.dloss : 1.f;
   const int count = a.counts && tid < a.E ? a.counts[tid] : 0;
   const bool live = in && (!a.mask || a.mask[t]);
-  float p[kMaxE / 4];
+  const int per = (a.E + 3) / 4, e0 = q * per;  // this thread's experts: e0 .. e0 + per - 1
+  const int mine = min(per, a.E - e0);
+  float p[Q];
 #pragma unroll
-  for (int i = 0; i < kMaxE / 4; ++i) {
-    const int e = q + 4 * i;
-    p[i] = in && (a.counts || all) && e < a.E ? a.scores[static_cast<int64_t>(e) * a.T + t] : 0.f;
-  }
+  for (int i = 0; i < Q; ++i)
+    p[i] = in && (a.counts || all) && i < mine
+               ? a.scores[static_cast<int64_t>(e0 + i) * a.T + t]
+               : 0.f;
   // The token's slots q and q + 4.
   int sel[2];
   float g[2], dg[2];
@@ -127,20 +132,24 @@ __global__ void __launch_bounds__(kDzThreads)
     f[tid] = loss ? static_cast<float>(count) / (static_cast<float>(n) * a.k) : 0.f;
   const float c = loss ? a.coef * dloss * a.E / n : 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxE / 4; ++i) {
-    z[tok][q + 4 * i] = 0.f;
+  for (int i = 0; i < Q; ++i)
+    if (i < mine) z[tok][e0 + i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < Q; ++i)
     if (!live) p[i] = 0.f;
-  }
 #pragma unroll
   for (int s = 0; s < 2; ++s)
     if (!live) sel[s] = -1, g[s] = dg[s] = 0.f;
-  if (TC)  // the tail past the third term stays zero
+  // What no expert's term fills stays zero (with three blocks of terms every
+  // place of a row that is read is written below, or here).
+  if (TC && a.E < 64)
     for (int i = tid; i < kRbTokens * LD / 8; i += kDzThreads)
       reinterpret_cast<uint4*>(rows_s)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   float mean = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxE / 4; ++i) mean = fmaf(f[q + 4 * i], p[i], mean);
+  for (int i = 0; i < Q; ++i)
+    if (i < mine) mean = fmaf(f[e0 + i], p[i], mean);
   part[0][q][tok] = fmaf(g[0], dg[0], g[1] * dg[1]);
   part[1][q][tok] = mean;
   __syncthreads();
@@ -149,29 +158,57 @@ __global__ void __launch_bounds__(kDzThreads)
   mean = (part[1][0][tok] + part[1][1][tok]) + (part[1][2][tok] + part[1][3][tok]);
   // The gates' terms at the selected experts, a quarter of the slots at a
   // time: the same expert may come twice, so only one thread adds at once.
-  for (int turn = 0; turn < 4; ++turn) {
-    if (q == turn)
+  if (a.dgate)
+    for (int turn = 0; turn < min(4, a.k); ++turn) {
+      if (q == turn)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (sel[s] >= 0 && sel[s] < a.E)
-          z[tok][sel[s]] += all ? g[s] * dg[s] : g[s] * (dg[s] - total / a.gate_scale);
-    __syncthreads();
-  }
+        for (int s = 0; s < 2; ++s)
+          if (sel[s] >= 0 && sel[s] < a.E)
+            z[tok][sel[s]] += all ? g[s] * dg[s] : g[s] * (dg[s] - total / a.gate_scale);
+      __syncthreads();
+    }
+  uint32_t hi2[Q / 2], mid2[Q / 2], lo2[Q / 2];  // TC: two experts' terms to a word
 #pragma unroll
-  for (int i = 0; i < kMaxE / 4; ++i) {
-    const int e = q + 4 * i;
-    if (e >= a.E) break;
-    float v = z[tok][e];
-    if (live && loss) v = fmaf(c * p[i], f[e] - mean, v);
-    if (live && all) v = fmaf(-p[i], total, v);
-    z[tok][e] = v;
+  for (int i = 0; i < Q; ++i) {
+    float v = 0.f;
+    if (i < mine) {
+      v = z[tok][e0 + i];
+      if (live && loss) v = fmaf(c * p[i], f[e0 + i] - mean, v);
+      if (live && all) v = fmaf(-p[i], total, v);
+      z[tok][e0 + i] = v;
+    }
     if (TC) {
       const float hi = bf16_round(v), rest = isfinite(hi) ? v - hi : 0.f;
-      const float mid = bf16_round(rest);
-      __nv_bfloat16* row = rows_s + tok * LD + e;
-      row[0] = __float2bfloat16(hi);
-      row[terms.stride] = __float2bfloat16(mid);
-      row[2 * terms.stride] = __float2bfloat16(rest - mid);
+      const float mid = bf16_round(rest), lo = rest - mid;
+      auto put = [&](uint32_t (&w)[Q / 2], float x) {
+        const uint32_t b = __bfloat16_as_ushort(__float2bfloat16(x));
+        w[i / 2] = i % 2 ? w[i / 2] | b << 16 : b;
+      };
+      put(hi2, hi);
+      put(mid2, mid);
+      put(lo2, lo);
+    }
+  }
+  if (TC) {
+    __nv_bfloat16* row = rows_s + tok * LD;
+    if (Q == kMaxE / 4 && per == Q) {
+      // Sixteen experts are 32 bytes of each of three 64-wide blocks.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4* at = reinterpret_cast<uint4*>(row + e0) + h;
+        at[0] = make_uint4(hi2[4 * h], hi2[4 * h + 1], hi2[4 * h + 2], hi2[4 * h + 3]);
+        at[8] = make_uint4(mid2[4 * h], mid2[4 * h + 1], mid2[4 * h + 2], mid2[4 * h + 3]);
+        at[16] = make_uint4(lo2[4 * h], lo2[4 * h + 1], lo2[4 * h + 2], lo2[4 * h + 3]);
+      }
+    } else {
+      uint16_t* at = reinterpret_cast<uint16_t*>(row) + e0;
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        if (i >= mine) continue;
+        at[i] = static_cast<uint16_t>(hi2[i / 2] >> (i % 2 * 16));
+        at[i + terms.stride] = static_cast<uint16_t>(mid2[i / 2] >> (i % 2 * 16));
+        at[i + 2 * terms.stride] = static_cast<uint16_t>(lo2[i / 2] >> (i % 2 * 16));
+      }
     }
   }
   __syncthreads();
@@ -187,12 +224,16 @@ __global__ void __launch_bounds__(kDzThreads)
   } else {
     float* out = static_cast<float*>(dz) + static_cast<int64_t>(t0) * EP;
     const int shift = __ffs(EP) - 1;      // EP is a power of two
-    for (int i = tid; i < rows * EP; i += kDzThreads) out[i] = z[i >> shift][i & (EP - 1)];
+    for (int i = tid; i < rows * EP; i += kDzThreads) {
+      const int e = i & (EP - 1);
+      out[i] = e < a.E ? z[i >> shift][e] : 0.f;
+    }
   }
   // tok is an expert here, q a quarter of the tokens.
   float s = 0.f;
+  if (tok < a.E)
 #pragma unroll
-  for (int r = 0; r < kRbTokens / 4; ++r) s += z[q * (kRbTokens / 4) + r][tok];
+    for (int r = 0; r < kRbTokens / 4; ++r) s += z[q * (kRbTokens / 4) + r][tok];
   part[0][q][tok] = s;
   __syncthreads();
   if (q == 0)
@@ -420,7 +461,11 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& a, moe_dtype dtype, c
                          dz_terms(a.E), static_cast<void*>(ws + p.dz), bias, sums.err,
                          sums.tickets, p.cols);
   };
-  const cudaError_t err = tc ? dz(route_dz_kernel<true>) : dz(route_dz_kernel<false>);
+  const cudaError_t err =
+      a.E <= 8    ? (tc ? dz(route_dz_kernel<true, 2>) : dz(route_dz_kernel<false, 2>))
+      : a.E <= 16 ? (tc ? dz(route_dz_kernel<true, 4>) : dz(route_dz_kernel<false, 4>))
+      : a.E <= 32 ? (tc ? dz(route_dz_kernel<true, 8>) : dz(route_dz_kernel<false, 8>))
+                  : (tc ? dz(route_dz_kernel<true, 16>) : dz(route_dz_kernel<false, 16>));
   if (err != cudaSuccess) return err;
   if (!a.dx && !a.dWg) return launch_kernel(route_bias_kernel, dim3(a.E), dim3(32), 0, s, 1, true, sums);
   return tc ? launch_route_products_tc(a, p, sums, s)

@@ -38,7 +38,7 @@ struct RouteBackwardPlan {
 // in order; `bias` are the dz blocks' column sums [blocks][kMaxE].
 struct RouteSums {
   const float* bias;
-  float* dw;          // [ranges, d, E]
+  float* dw;          // [ranges, d, E] (three blocks of terms: [ranges, cols] parts)
   int32_t* err;
   uint32_t* tickets;
   float* dWg;         // null: not wanted
@@ -109,5 +109,6 @@ cudaError_t launch_route_products_tc(const RouteBackwardArgs& a, const RouteBack
                                      const RouteSums& sums, cudaStream_t s);
 constexpr int kRbTcCols = 128;   // columns and tokens of one tile
 constexpr int kRbTcTokens = 128;
+constexpr int kRbPartBytes = 32768;  // a column block's dW_g of one range, three blocks of terms
 
 }  // namespace moe

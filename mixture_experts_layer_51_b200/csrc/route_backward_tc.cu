@@ -42,6 +42,8 @@ constexpr int kDwCol = 256;           // dW_g's first column in tensor memory
 // to ten times what sums that round are off.
 constexpr int kFlush = 4;
 constexpr int kSmem = 14 * kUnit + 2048;  // + control block and alignment
+constexpr int kPartBytes = kRbPartBytes;
+static_assert(kPartBytes == kEpilogue * 32 * 4, "32 floats a thread");
 
 // NB: 64-element blocks of a dz row.  Stages x (2 + NB), W_g blocks and
 // staging units add up to the same 14 blocks of shared memory.
@@ -446,36 +448,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) give_up(p, c, kErrTimeoutEpilogue);
     if (p.want_dw) {
-      if (epilogue_all(ok)) {
-        // The last flush came after the last MMA: the ring is idle, and the
-        // rows go through it so that they leave in whole lines.
-        float* rows = reinterpret_cast<float*>(smem);
-        constexpr int LD = 2 * ACC + 1;
+      ok = epilogue_all(ok);
+      const int block = blockIdx.x % p.cols, ncols = min(kRbTcCols, p.d - c0), n = ncols * p.E;
+      // The block's rows go through the ring, which is idle after the last
+      // flush, so that they leave in whole lines: f(i, value) for element i of
+      // [columns][E].
+      constexpr int LD = 2 * ACC + 1;
+      float* rows = reinterpret_cast<float*>(smem);
+      auto through_ring = [&](auto f) {
 #pragma unroll
         for (int e = 0; e < ACC; ++e) rows[row * LD + group * ACC + e] = acc[e];
         epilogue_sync();
-        const int n = min(kRbTcCols, p.d - c0) * p.E;
-        float* out = p.sums.dw + (static_cast<int64_t>(range) * p.d + c0) * p.E;
         int r = et / p.E, e = et % p.E;
         const int dr = kEpilogue / p.E, de = kEpilogue % p.E;
         for (int i = et; i < n; i += kEpilogue) {
           const float* at = rows + r * LD + e;
-          out[i] = NB == 3 ? at[0] : at[2 * p.stride] + at[p.stride] + at[0];
+          f(i, NB == 3 ? at[0] : at[2 * p.stride] + at[p.stride] + at[0]);
           r += dr;
           e += de;
           if (e >= p.E) e -= p.E, ++r;
         }
+      };
+      // A range's part: three blocks of terms are already one value an
+      // expert, so the registers leave as they are, 16 bytes a thread; with
+      // fewer, the terms are added first.
+      float4* mine = reinterpret_cast<float4*>(p.sums.dw) + block * (kPartBytes / 16) + et;
+      const int64_t plane = static_cast<int64_t>(p.cols) * (kPartBytes / 16);
+      if (ok && NB == 3) {
+#pragma unroll
+        for (int j = 0; j < ACC / 4; ++j)
+          mine[range * plane + j * kEpilogue] =
+              make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+      } else if (ok) {
+        float* out = p.sums.dw + (static_cast<int64_t>(range) * p.d + c0) * p.E;
+        through_ring([&](int i, float v) { out[i] = v; });
       }
       __threadfence();
       epilogue_sync();
       if (et == 0)
-        c.last = atomicAdd(p.sums.tickets + blockIdx.x % p.cols, 1u) + 1 ==
-                 static_cast<uint32_t>(p.ranges);
+        c.last = atomicAdd(p.sums.tickets + block, 1u) + 1 == static_cast<uint32_t>(p.ranges);
       epilogue_sync();
       if (c.last) {
         __threadfence();
-        sum_ranges(p.sums, c0, min(kRbTcCols, p.d - c0), et, kEpilogue,
-                   reinterpret_cast<float4*>(smem), epilogue_sync);
+        if (NB == 3) {
+          const bool failed = *static_cast<volatile int32_t*>(p.sums.err) != 0;
+          float own[ACC];
+#pragma unroll
+          for (int e = 0; e < ACC; ++e) own[e] = acc[e], acc[e] = 0.f;
+#pragma unroll 2
+          for (int r = 0; r < p.ranges; ++r) {
+#pragma unroll
+            for (int j = 0; j < ACC / 4; ++j) {
+              const float4 v = r == range ? make_float4(own[4 * j], own[4 * j + 1], own[4 * j + 2],
+                                                        own[4 * j + 3])
+                                          : __ldcg(mine + r * plane + j * kEpilogue);
+              acc[4 * j] += v.x, acc[4 * j + 1] += v.y, acc[4 * j + 2] += v.z,
+                  acc[4 * j + 3] += v.w;
+            }
+          }
+          float* out = p.sums.dWg + static_cast<int64_t>(c0) * p.E;
+          through_ring(
+              [&](int i, float v) { out[i] = failed ? __int_as_float(0x7fc00000) : v; });
+        } else {
+          sum_ranges(p.sums, c0, ncols, et, kEpilogue, reinterpret_cast<float4*>(smem),
+                     epilogue_sync);
+        }
       }
     }
   }
