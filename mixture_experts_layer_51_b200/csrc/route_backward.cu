@@ -23,7 +23,8 @@
 namespace moe {
 namespace {
 
-constexpr int kDzThreads = 4 * kRbTokens;
+constexpr int kDzParts = 8;        // threads of a token in the dz kernel
+constexpr int kDzThreads = kDzParts * kRbTokens;
 constexpr int kCols = 64;          // fp32 products: columns of one CTA,
 constexpr int kTile = 64;          // tokens of one tile
 constexpr int kThreads = 256;
@@ -71,15 +72,34 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   return p;
 }
 
-__device__ __forceinline__ float bf16_round(float v) {
-  return __bfloat162float(__float2bfloat16(v));
+// v = hi + mid + lo, each with a bf16's eight significant bits (in the upper
+// half of its fp32 pattern): the nearest, then the nearest of what is left,
+// whose rest is exact.  Infinities and NaN stay in hi.
+struct Terms {
+  uint32_t hi, mid;
+  float lo;
+};
+__device__ __forceinline__ Terms split(float v) {
+  constexpr uint32_t kExp = 0x7f800000u;
+  const uint32_t u = __float_as_uint(v), up = u + 0x8000u;
+  const bool finite = (u & kExp) != kExp;
+  Terms t;  // next to the largest values, hi is cut instead of rounded up
+  t.hi = (finite && (up & kExp) != kExp ? up : u) & 0xffff0000u;
+  const float rest = finite ? v - __uint_as_float(t.hi) : 0.f;
+  t.mid = (__float_as_uint(rest) + 0x8000u) & 0xffff0000u;
+  t.lo = rest - __uint_as_float(t.mid);
+  return t;
+}
+// The upper halves of two words, `a`'s below `b`'s.
+__device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
+  return __byte_perm(a, b, 0x7632);
 }
 
-// dz of 64 tokens, four threads a token (each a quarter of the experts, kept
+// dz of 32 tokens, eight threads a token (each an eighth of the experts, kept
 // in registers so that the scores are read once), and its column sums.  TC:
 // dz leaves as bf16 terms, else as fp32 rows of EP; either way by way of
 // shared memory, in whole 16-byte pieces of contiguous rows.  Q: experts a
-// thread has room for (a quarter of E, rounded up to a power of two).
+// thread has room for (an eighth of E, rounded up to a power of two).
 template <bool TC, int Q>
 __global__ void __launch_bounds__(kDzThreads)
     route_dz_kernel(const RouteBackwardArgs a, int EP, DzTerms terms, void* __restrict__ dz,
@@ -90,7 +110,10 @@ __global__ void __launch_bounds__(kDzThreads)
   __shared__ float z[kRbTokens][kMaxE + 1];
   __shared__ __align__(16) __nv_bfloat16 rows_s[TC ? kRbTokens * LD : 8];
   __shared__ float f[kMaxE];
-  __shared__ float part[2][4][kRbTokens];
+  __shared__ float part[2][kDzParts][kRbTokens];
+  __shared__ int32_t sel_s[kMaxK][kRbTokens];
+  __shared__ float term_s[kMaxK][kRbTokens];
+  __shared__ float sum_s[4][kMaxE];
   const int tid = threadIdx.x, tok = tid % kRbTokens, q = tid / kRbTokens;
   const int t0 = blockIdx.x * kRbTokens, t = t0 + tok;
   pdl_wait();
@@ -107,7 +130,7 @@ __global__ void __launch_bounds__(kDzThreads)
   const float dloss = a.counts && a.dloss ? *a.dloss : 1.f;
   const int count = a.counts && tid < a.E ? a.counts[tid] : 0;
   const bool live = in && (!a.mask || a.mask[t]);
-  const int per = (a.E + 3) / 4, e0 = q * per;  // this thread's experts: e0 .. e0 + per - 1
+  const int per = (a.E + kDzParts - 1) / kDzParts, e0 = q * per;  // this thread's experts: e0 .. e0 + per - 1
   const int mine = min(per, a.E - e0);
   float p[Q];
 #pragma unroll
@@ -115,18 +138,12 @@ __global__ void __launch_bounds__(kDzThreads)
     p[i] = in && (a.counts || all) && i < mine
                ? a.scores[static_cast<int64_t>(e0 + i) * a.T + t]
                : 0.f;
-  // The token's slots q and q + 4.
-  int sel[2];
-  float g[2], dg[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int j = q + 4 * s;
-    const bool use = in && a.dgate && j < a.k;
-    const int64_t at = static_cast<int64_t>(t) * a.k + j;
-    sel[s] = use ? a.idx[at] : -1;
-    g[s] = use ? a.gate[at] : 0.f;
-    dg[s] = use ? a.dgate[at] : 0.f;
-  }
+  // The token's slot q.
+  static_assert(kMaxK <= kDzParts, "a slot a thread");
+  const bool slot = in && a.dgate && q < a.k;
+  const int64_t at = static_cast<int64_t>(t) * a.k + q;
+  const int sel = slot ? a.idx[at] : -1;
+  float g = slot ? a.gate[at] : 0.f, dg = slot ? a.dgate[at] : 0.f;
   const bool loss = n > 0;
   if (tid < kMaxE)
     f[tid] = loss ? static_cast<float>(count) / (static_cast<float>(n) * a.k) : 0.f;
@@ -137,9 +154,7 @@ __global__ void __launch_bounds__(kDzThreads)
 #pragma unroll
   for (int i = 0; i < Q; ++i)
     if (!live) p[i] = 0.f;
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (!live) sel[s] = -1, g[s] = dg[s] = 0.f;
+  if (!live) g = dg = 0.f;
   // What no expert's term fills stays zero (with three blocks of terms every
   // place of a row that is read is written below, or here).
   if (TC && a.E < 64)
@@ -150,56 +165,56 @@ __global__ void __launch_bounds__(kDzThreads)
 #pragma unroll
   for (int i = 0; i < Q; ++i)
     if (i < mine) mean = fmaf(f[e0 + i], p[i], mean);
-  part[0][q][tok] = fmaf(g[0], dg[0], g[1] * dg[1]);
+  part[0][q][tok] = g * dg;
   part[1][q][tok] = mean;
   __syncthreads();
-  const float total =
-      (part[0][0][tok] + part[0][1][tok]) + (part[0][2][tok] + part[0][3][tok]);
-  mean = (part[1][0][tok] + part[1][1][tok]) + (part[1][2][tok] + part[1][3][tok]);
-  // The gates' terms at the selected experts, a quarter of the slots at a
-  // time: the same expert may come twice, so only one thread adds at once.
-  if (a.dgate)
-    for (int turn = 0; turn < min(4, a.k); ++turn) {
-      if (q == turn)
+  float total = 0.f;
+  mean = 0.f;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          if (sel[s] >= 0 && sel[s] < a.E)
-            z[tok][sel[s]] += all ? g[s] * dg[s] : g[s] * (dg[s] - total / a.gate_scale);
-      __syncthreads();
-    }
-  uint32_t hi2[Q / 2], mid2[Q / 2], lo2[Q / 2];  // TC: two experts' terms to a word
+  for (int i = 0; i < kDzParts; ++i) total += part[0][i][tok], mean += part[1][i][tok];
+  // The gates' terms at the selected experts, slot after slot by one thread a
+  // token: the same expert may come twice.
+  if (a.dgate) {
+    sel_s[q][tok] = live && sel < a.E ? sel : -1;
+    term_s[q][tok] = all ? g * dg : g * (dg - total / a.gate_scale);
+    __syncthreads();
+    if (q == 0)
+      for (int j = 0; j < a.k; ++j)
+        if (sel_s[j][tok] >= 0) z[tok][sel_s[j][tok]] += term_s[j][tok];
+  }
+  __syncthreads();
+  constexpr int W = (Q + 1) / 2;
+  uint32_t hi2[W], mid2[W], lo2[W];  // TC: two experts' terms to a word
 #pragma unroll
-  for (int i = 0; i < Q; ++i) {
-    float v = 0.f;
-    if (i < mine) {
-      v = z[tok][e0 + i];
-      if (live && loss) v = fmaf(c * p[i], f[e0 + i] - mean, v);
-      if (live && all) v = fmaf(-p[i], total, v);
-      z[tok][e0 + i] = v;
+  for (int i = 0; i < Q; i += 2) {
+    float v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v[h] = 0.f;
+      if (i + h >= Q || i + h >= mine) continue;
+      const float pe = p[(i + h) % Q];
+      v[h] = z[tok][e0 + i + h];
+      if (live && loss) v[h] = fmaf(c * pe, f[e0 + i + h] - mean, v[h]);
+      if (live && all) v[h] = fmaf(-pe, total, v[h]);
     }
     if (TC) {
-      const float hi = bf16_round(v), rest = isfinite(hi) ? v - hi : 0.f;
-      const float mid = bf16_round(rest), lo = rest - mid;
-      auto put = [&](uint32_t (&w)[Q / 2], float x) {
-        const uint32_t b = __bfloat16_as_ushort(__float2bfloat16(x));
-        w[i / 2] = i % 2 ? w[i / 2] | b << 16 : b;
-      };
-      put(hi2, hi);
-      put(mid2, mid);
-      put(lo2, lo);
+      const Terms x = split(v[0]), y = split(v[1]);
+      hi2[i / 2] = upper_halves(x.hi, y.hi);
+      mid2[i / 2] = upper_halves(x.mid, y.mid);
+      lo2[i / 2] = upper_halves(__float_as_uint(x.lo), __float_as_uint(y.lo));
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (i + h < Q && i + h < mine) z[tok][e0 + i + h] = v[h];
   }
   if (TC) {
     __nv_bfloat16* row = rows_s + tok * LD;
-    if (Q == kMaxE / 4 && per == Q) {
-      // Sixteen experts are 32 bytes of each of three 64-wide blocks.
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4* at = reinterpret_cast<uint4*>(row + e0) + h;
-        at[0] = make_uint4(hi2[4 * h], hi2[4 * h + 1], hi2[4 * h + 2], hi2[4 * h + 3]);
-        at[8] = make_uint4(mid2[4 * h], mid2[4 * h + 1], mid2[4 * h + 2], mid2[4 * h + 3]);
-        at[16] = make_uint4(lo2[4 * h], lo2[4 * h + 1], lo2[4 * h + 2], lo2[4 * h + 3]);
-      }
+    if (Q == 8 && per == Q) {
+      // Eight experts are 16 bytes of each of three 64-wide blocks.
+      uint4* at = reinterpret_cast<uint4*>(row + e0);
+      at[0] = make_uint4(hi2[0], hi2[1 % W], hi2[2 % W], hi2[3 % W]);
+      at[8] = make_uint4(mid2[0], mid2[1 % W], mid2[2 % W], mid2[3 % W]);
+      at[16] = make_uint4(lo2[0], lo2[1 % W], lo2[2 % W], lo2[3 % W]);
     } else {
       uint16_t* at = reinterpret_cast<uint16_t*>(row) + e0;
 #pragma unroll
@@ -229,16 +244,17 @@ __global__ void __launch_bounds__(kDzThreads)
       out[i] = e < a.E ? z[i >> shift][e] : 0.f;
     }
   }
-  // tok is an expert here, q a quarter of the tokens.
+  // Column sums: 64 threads, one an expert, on each quarter of the tokens.
+  const int e = tid % kMaxE, quarter = tid / kMaxE;
   float s = 0.f;
-  if (tok < a.E)
+  if (e < a.E)
 #pragma unroll
-    for (int r = 0; r < kRbTokens / 4; ++r) s += z[q * (kRbTokens / 4) + r][tok];
-  part[0][q][tok] = s;
+    for (int r = 0; r < kRbTokens / 4; ++r) s += z[quarter * (kRbTokens / 4) + r][e];
+  sum_s[quarter][e] = s;
   __syncthreads();
-  if (q == 0)
-    bias_part[static_cast<int64_t>(blockIdx.x) * kMaxE + tok] =
-        (part[0][0][tok] + part[0][1][tok]) + (part[0][2][tok] + part[0][3][tok]);
+  if (quarter == 0)
+    bias_part[static_cast<int64_t>(blockIdx.x) * kMaxE + e] =
+        (sum_s[0][e] + sum_s[1][e]) + (sum_s[2][e] + sum_s[3][e]);
 }
 
 // Both products of an fp32 layer, on fp32 FMA.  A CTA owns 64 columns and a
@@ -462,10 +478,10 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& a, moe_dtype dtype, c
                          sums.tickets, p.cols);
   };
   const cudaError_t err =
-      a.E <= 8    ? (tc ? dz(route_dz_kernel<true, 2>) : dz(route_dz_kernel<false, 2>))
-      : a.E <= 16 ? (tc ? dz(route_dz_kernel<true, 4>) : dz(route_dz_kernel<false, 4>))
-      : a.E <= 32 ? (tc ? dz(route_dz_kernel<true, 8>) : dz(route_dz_kernel<false, 8>))
-                  : (tc ? dz(route_dz_kernel<true, 16>) : dz(route_dz_kernel<false, 16>));
+      a.E <= 8    ? (tc ? dz(route_dz_kernel<true, 1>) : dz(route_dz_kernel<false, 1>))
+      : a.E <= 16 ? (tc ? dz(route_dz_kernel<true, 2>) : dz(route_dz_kernel<false, 2>))
+      : a.E <= 32 ? (tc ? dz(route_dz_kernel<true, 4>) : dz(route_dz_kernel<false, 4>))
+                  : (tc ? dz(route_dz_kernel<true, 8>) : dz(route_dz_kernel<false, 8>));
   if (err != cudaSuccess) return err;
   if (!a.dx && !a.dWg) return launch_kernel(route_bias_kernel, dim3(a.E), dim3(32), 0, s, 1, true, sums);
   return tc ? launch_route_products_tc(a, p, sums, s)

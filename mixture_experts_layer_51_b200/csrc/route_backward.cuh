@@ -7,7 +7,7 @@
 
 namespace moe {
 
-constexpr int kRbTokens = 64;    // tokens of one dz block
+constexpr int kRbTokens = 32;    // tokens of one dz block
 constexpr int kRbSms = 148;      // what grids are sized for (any GPU runs them)
 
 // dz as the tensor cores read it: bf16 terms hi + mid + lo of every value
