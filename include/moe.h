@@ -1,6 +1,7 @@
 /*
  * moe.h -- C ABI of libmoe.so: the forward pass of one token-choice
- * Mixture-of-Experts FFN layer on an NVIDIA B200 (sm_100a).
+ * Mixture-of-Experts FFN layer on an NVIDIA B200 (sm_100a), and what stands
+ * around the experts' products when it is trained.
  *
  * The layer (pages: "How do Mixture of Expert Models Work?", section "The
  * Math Behind MoEs"; "[Paper Club] Upcycling Large Language Models into
@@ -555,8 +556,10 @@ moe_status moe_balance_loss(const float* scores, const int32_t* idx, const uint8
  *   rounded once (dx_acc [T, d] (dtype) or NULL for 0; dx may be dx_acc; a
  *   padding token's row is its dx_acc); dWg [d, E] fp32 = x^T dz; dbias [E]
  *   fp32 = sum over the tokens of dz.  x may be NULL without dWg, Wg without
- *   dx.  T == 0 gives dWg = dbias = 0.
- *   ws: at least moe_route_backward_workspace_bytes(T, d, E, dtype). */
+ *   dx.  N == 0 adds nothing from the loss; T == 0 gives dWg = dbias = 0.
+ *   ws: at least moe_route_backward_workspace_bytes(T, d, E, dtype).  With
+ *   T > 0 its first int32 is an error word, written by every call: 0, or the
+ *   bits of a kernel that gave up on a bounded wait (dWg is NaN then). */
 size_t moe_route_backward_workspace_bytes(int32_t T, int32_t d, int32_t E, moe_dtype dtype);
 moe_status moe_route_backward(const void* x, const void* Wg, const float* scores,
                               const int32_t* idx, const float* gate, const float* dgate,

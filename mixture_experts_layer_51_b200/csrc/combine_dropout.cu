@@ -99,11 +99,12 @@ __device__ __forceinline__ void keep_masks(const uint32_t (&w)[4], uint32_t thre
 // Warps of a CTA sharing one token's row (1, 2, 4 or 8): this warp's token,
 // and which of the token's warps it is.
 struct Place {
-  int t, part;
+  int64_t t;
+  int part;
 };
 __device__ __forceinline__ Place place(int wpt) {
   const int warp = threadIdx.x >> 5;
-  return {static_cast<int>(blockIdx.x) * (kCdWarps / wpt) + warp / wpt, warp % wpt};
+  return {static_cast<int64_t>(blockIdx.x) * (kCdWarps / wpt) + warp / wpt, warp % wpt};
 }
 
 // The token's rows and gates, in every lane (row -1: no such slot).

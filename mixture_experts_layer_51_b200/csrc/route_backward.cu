@@ -288,13 +288,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int cols = min(kCols, a.d - c0);
   const bool in = 4 * cg < cols;             // columns come in eights
   const int64_t col = c0 + 4 * cg;
-  const int t0 = static_cast<int>(static_cast<int64_t>(blockIdx.y) * tiles / ranges) * kTile;
-  const int t1 = min(a.T, static_cast<int>(static_cast<int64_t>(blockIdx.y + 1) * tiles / ranges) *
-                              kTile);
+  // Unsigned: the end of the last tile may pass 2^31.
+  const uint32_t t0 = static_cast<uint32_t>(static_cast<int64_t>(blockIdx.y) * tiles / ranges) * kTile;
+  const uint32_t t1 = min(static_cast<uint32_t>(a.T),
+                          static_cast<uint32_t>(static_cast<int64_t>(blockIdx.y + 1) * tiles /
+                                                ranges) * kTile);
   pdl_wait();
   pdl_trigger();
-  auto load = [&](int tb, int st) {
-    const int rows = min(kTile, t1 - tb);
+  auto load = [&](uint32_t tb, int st) {
+    const int rows = min(static_cast<uint32_t>(kTile), t1 - tb);
     if (a.dWg)
 #pragma unroll
       for (int r = tid / 16; r < kTile; r += kThreads / 16) {
@@ -327,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int eg = tid / 16 % EG, tg = tid / (16 * EG);
   float acc[4][4] = {};
   int st = 0;
-  for (int tb = t0; tb < t1; tb += kTile, st ^= 1) {
-    const int rows = min(kTile, t1 - tb);
+  for (uint32_t tb = t0; tb < t1; tb += kTile, st ^= 1) {
+    const int rows = min(static_cast<uint32_t>(kTile), t1 - tb);
     if (tb + kTile < t1)
       load(tb + kTile, st ^ 1);
     else

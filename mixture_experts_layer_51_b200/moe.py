@@ -660,8 +660,9 @@ class MoELayer:
         balance loss [1] weighted by coef (mask: see moe_balance_loss), and
         ``step``, the dict of intermediates that backward_combine and
         backward_router read (xp, h, o, offsets and kept_counts among them,
-        for a backward pass of the experts).  x, gates and rng are held, not
-        copied."""
+        for a backward pass of the experts).  x and rng are held, not copied:
+        neither may change before the backward pass."""
+        _tensor(x, "x", self.dtype, (x.shape[0], self.d), self.device)
         idx, gate, _ = moe_route(x, self.Wg, self.bias, self.k, gating=self.gating,
                                  gate_scale=self.gate_scale)
         scores = moe_expert_choice_route(x, self.Wg, self.bias)
@@ -694,6 +695,7 @@ class MoELayer:
         own backward pass; dx then holds both."""
         dx_acc = None
         if dxp is not None and "dx" in outputs:
+            _tensor(dxp, "dxp", self.dtype, step["xp"].shape, self.device)
             dx_acc = moe_unpermute_combine(dxp, step["pos"], torch.ones_like(step["gate"]),
                                            step["x"].dtype)
         return moe_route_backward(step["x"], self.Wg, step["idx"], step["gate"], step["dgate"],

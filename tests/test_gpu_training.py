@@ -51,6 +51,8 @@ def _mask(g, T, kind):
     m = torch.rand(T, generator=g, device=DEV) > 0.3
     if kind == "none":
         m[:] = False
+    if kind == "tail":
+        m[:] = torch.arange(T, device=DEV) < T // 3
     return m if kind != "bytes" else m.to(torch.uint8)
 
 
@@ -129,6 +131,17 @@ ROUTE = [
     (5000, 64, 12, 2, "bf16", "topk_softmax", 1.0, True, True, None, True),
     (3001, 4104, 9, 2, "bf16", "topk_softmax", 1.0, True, True, "some", False),
     (20000, 72, 64, 8, "bf16", "softmax_topk", 1.0, True, True, "some", True),
+    # the widths at which the terms of dz take another block
+    (260, 136, 21, 3, "bf16", "softmax_topk", 1.0, True, True, "some", True),
+    (260, 136, 22, 3, "bf16", "topk_softmax", 1.0, True, True, None, False),
+    (260, 136, 42, 3, "bf16", "softmax_topk", 1.0, True, True, None, True),
+    (260, 136, 43, 3, "bf16", "topk_softmax", 1.0, True, True, "some", False),
+    (700, 320, 61, 8, "bf16", "softmax_topk", 1.0, True, True, "some", True),
+    (700, 320, 63, 7, "fp32", "softmax_topk", 1.0, True, True, "some", True),
+    # ranges of many tiles, three blocks of terms
+    (6000, 2056, 64, 8, "bf16", "softmax_topk", 1.0, True, True, "some", True),
+    # a padded batch whose tail is all padding (whole tiles of it)
+    (1500, 264, 8, 2, "bf16", "topk_softmax", 1.0, True, True, "tail", True),
 ]
 
 
@@ -533,6 +546,71 @@ def test_binding_refusals_on_the_gpu():
         M.moe_route_backward(**b, outputs=("dx", "dx"))
     with pytest.raises(M.MoeError):
         M.moe_route_backward(**b, ws=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
+def test_the_error_word_is_written_and_clear():
+    a = _route_case(*ROUTE[11])
+    need = M.moe_route_backward_workspace_bytes(1000, 1024, 8, torch.bfloat16)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    _check_route(a, M.moe_route_backward(**a, ws=ws))
+    assert int(ws[:4].view(torch.int32)) == 0
+
+
+@pytest.mark.parametrize("v", [3.0e38, 3.4e38, -3.4e38, 1e-39, float("inf"), float("nan")])
+def test_route_backward_at_the_ends_of_the_range(v):
+    """Gate gradients so large, small or not finite that their terms in bf16
+    need care: one token, one expert, against the fp64 product."""
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device=DEV)
+    x[1, 3] = 1.0
+    Wg = torch.zeros((64, 8), dtype=torch.bfloat16, device=DEV)
+    Wg[:, 2] = 0.5
+    idx = torch.full((4, 1), 2, dtype=torch.int32, device=DEV)
+    gate, dgate = torch.zeros((4, 1), device=DEV), torch.zeros((4, 1), device=DEV)
+    scores = torch.zeros((8, 4), device=DEV)
+    gate[1], dgate[1] = 1.0, v  # softmax over all with p = 0 elsewhere: dz = g dg
+    got = M.moe_route_backward(x, Wg, idx, gate, dgate, scores, gating="softmax_topk")
+    want = torch.zeros((64, 8), dtype=torch.float64)
+    want[3, 2] = v
+    dWg, dx = got["dWg"].double().cpu(), got["dx"].double().cpu()
+    if v != v or abs(v) == float("inf"):
+        assert torch.equal(dWg[3, 2].isnan() | (dWg[3, 2] == v), torch.tensor(True))
+        assert bool((dx[1].isnan() | (dx[1] == v)).all())
+        return
+    # three terms hold v; those below the smallest normal number may be lost
+    assert abs(float(dWg[3, 2]) - v) <= 2 * U32 * abs(v) + 2.0 ** -126
+    half = torch.full((64,), v / 2, dtype=torch.float64)
+    assert torch.all((dx[1] - half).abs() <= (2.0 ** -8 + 2.0 ** -15) * half.abs() + 2.0 ** -126)
+    assert not dx[[0, 2, 3]].any()
+
+
+def test_a_training_step_of_an_empty_batch():
+    from mixture_experts_layer_51_b200.workloads import Workload, make_inputs
+    w = Workload("t", T=8, d=64, E=4, k=2, H=64, act="swiglu", dtype="bf16", cf=0.0, seed=9)
+    t = make_inputs(w, DEV)
+    layer = M.MoELayer(t["Wg"], t["bias"], t["W1"], t["W3"], t["W2"], w.k, w.cf, w.act)
+    x = t["x"][:0]
+    y, loss, step = layer.forward_train(x, coef=0.1)
+    assert y.shape == (0, 64) and float(loss) == 0
+    layer.backward_combine(step, y)
+    grads = layer.backward_router(step)
+    assert not grads["dWg"].any() and not grads["dbias"].any() and grads["dx"].shape == (0, 64)
+
+
+def test_the_step_refuses_what_it_cannot_read():
+    from mixture_experts_layer_51_b200.workloads import Workload, make_inputs
+    w = Workload("t", T=40, d=64, E=4, k=2, H=64, act="swiglu", dtype="bf16", cf=0.0, seed=9)
+    t = make_inputs(w, DEV)
+    layer = M.MoELayer(t["Wg"], t["bias"], t["W1"], t["W3"], t["W2"], w.k, w.cf, w.act)
+    with pytest.raises(ValueError):
+        layer.forward_train(torch.cat([t["x"], t["x"]], 1)[:, :64])
+    with pytest.raises(TypeError):
+        layer.forward_train(t["x"].float())
+    with pytest.raises(M.MoeError):
+        layer.forward_train(t["x"], p=0.5)  # no generator
+    _, _, step = layer.forward_train(t["x"])
+    layer.backward_combine(step, t["x"])
+    with pytest.raises(ValueError):
+        layer.backward_router(step, dxp=step["xp"][:-128])
 
 
 @pytest.mark.parametrize("gating,priority,cf,dtype,act", [
