@@ -101,7 +101,7 @@ __device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
 // shared memory, in whole 16-byte pieces of contiguous rows.  Q: experts a
 // thread has room for (an eighth of E, rounded up to a power of two).
 template <bool TC, int Q>
-__global__ void __launch_bounds__(kDzThreads)
+__global__ void __launch_bounds__(kDzThreads, 4)
     route_dz_kernel(const RouteBackwardArgs a, int EP, DzTerms terms, void* __restrict__ dz,
                     float* __restrict__ bias_part, int32_t* __restrict__ err,
                     uint32_t* __restrict__ tickets, int ntickets) {
@@ -172,15 +172,25 @@ __global__ void __launch_bounds__(kDzThreads)
   mean = 0.f;
 #pragma unroll
   for (int i = 0; i < kDzParts; ++i) total += part[0][i][tok], mean += part[1][i][tok];
-  // The gates' terms at the selected experts, slot after slot by one thread a
-  // token: the same expert may come twice.
+  // The gates' terms at the selected experts.  The same expert may come twice:
+  // the first of its slots adds them all, in order.
   if (a.dgate) {
-    sel_s[q][tok] = live && sel < a.E ? sel : -1;
-    term_s[q][tok] = all ? g * dg : g * (dg - total / a.gate_scale);
+    const bool use = live && sel >= 0 && sel < a.E;
+    const float rest = a.gate_scale == 1.f ? total : total / a.gate_scale;
+    sel_s[q][tok] = use ? sel : -1;
+    term_s[q][tok] = all ? g * dg : g * (dg - rest);
     __syncthreads();
-    if (q == 0)
-      for (int j = 0; j < a.k; ++j)
-        if (sel_s[j][tok] >= 0) z[tok][sel_s[j][tok]] += term_s[j][tok];
+    if (use) {
+      float sum = 0.f;
+      bool first = true;
+#pragma unroll
+      for (int j = 0; j < kMaxK; ++j) {  // slots past k are -1
+        const bool same = sel_s[j][tok] == sel;
+        if (same && j < q) first = false;
+        if (same) sum += term_s[j][tok];
+      }
+      if (first) z[tok][sel] = sum;
+    }
   }
   __syncthreads();
   constexpr int W = (Q + 1) / 2;
