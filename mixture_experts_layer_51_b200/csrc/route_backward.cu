@@ -16,7 +16,16 @@
 // range is done (bf16: tensor cores, route_backward_tc.cu; fp32: FMA, here).
 // The last range of a column block to finish adds all of the block's ranges
 // in order, and one warp an expert the dz blocks' column sums, so no sum
-// depends on scheduling (no floating-point atomics).
+// depends on scheduling (no floating-point atomics).  Adding them in a third
+// launch took as long on the GPU (56.8 and 56.0 us on the fine-grained shape)
+// and 2 us more of the host.
+//
+// dz is a launch of its own because every column block needs it: 5.6 MB of
+// scores and gates in, 128 to 384 bytes a token out (bf16 terms), 7 us for
+// 16384 tokens of 64 experts beside the products' first loads, of which about
+// 3 are its arithmetic.  Blocks of 32 tokens with eight threads a token beat
+// 64 with four (48.3 -> 46.7 us for the whole pass), and 64 registers a thread
+// beat 32 (46.7 -> 44.7 us).
 
 #include "route_backward.cuh"
 
