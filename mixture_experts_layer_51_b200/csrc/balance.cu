@@ -9,16 +9,18 @@
 //
 // Bound by reading the scores once, and for small batches by launches and
 // round trips to memory.  So a batch of up to 64 KB (scores and indices) is
-// one CTA's, one of up to 512 KB a cluster's of eight CTAs, whose first adds
+// one CTA's, one of up to 768 KB a cluster's of eight CTAs, whose first adds
 // the others' sums out of their shared memory, and a larger one takes a CTA on
 // every SM and a second launch that adds the slices from the workspace.
 //
-// Measured back to back in a graph on one B200: 256 tokens of 4 experts 3.6 us
-// (4.4 as a cluster), 80 KB 4.6 us as a cluster (6.9 in one CTA), 295 KB 5.5
-// (6.1 in two launches), 1.2 MB 6.2 in two launches (7.7 as a cluster),
-// 100003 tokens of 64 experts with a mask (29 MB) 12.1 us; reading that takes
-// 4.4 us at 6.56 TB/s, the rest is two launches, two rounds of loads and the
-// last sums.
+// Measured back to back in a graph on one B200 (with eight scores a lane on
+// their way, which costs small batches 0.5 us and large ones nothing): 5 KB
+// 3.9 us in one CTA, 4.8 as a cluster; 147 KB 5.4 and 4.9; 590 KB 4.9 as a
+// cluster, 5.7 in two launches; 1.2 MB 6.4 and 5.7.  As built: 256 tokens of 4
+// experts 3.3 us, 8192 of 8 5.1 us, 100003 of 64 with a mask (29 MB) 9.0 us;
+// reading that takes 4.4 us at 6.56 TB/s, the rest is two launches and the
+// last sums.  The mask as one word of ballots for 32 tokens, instead of a byte
+// beside every score: 12.1 -> 8.7 us.
 
 #include "moe_internal.cuh"
 
@@ -27,12 +29,13 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+static_assert(kWarps == 32, "a warp adds up the warps");
 constexpr int kCluster = 8;
 constexpr int64_t kOneBytes = 1 << 16;      // scores and indices that one CTA takes,
-constexpr int64_t kClusterBytes = 1 << 19;  // and one cluster
+constexpr int64_t kClusterBytes = 3 << 18;  // and one cluster
 constexpr int kMaxSlices = 148;     // one CTA on each SM
 constexpr int kMinSlice = 256;      // tokens
-constexpr int kBatch = 12;          // scores a lane has on their way per expert
+constexpr int kBatch = 4;           // scores a lane has on their way per expert
 
 // A slice's sums: S_e, counts_e, N.
 struct Partial {
@@ -52,63 +55,63 @@ Slices slices(int T) {
 }
 
 // The sums over tokens t0 .. t1 - 1 into `out` (shared memory), by the whole
-// CTA.  A warp takes an expert's scores, 32 kBatch tokens at a time; with fewer
-// than 32 experts several warps share one, each with a part of the tokens.
+// CTA, 1024 tokens at a time: thread i asks for its token's mask and experts,
+// a warp for an expert's scores, 32 kBatch tokens at a time (with fewer than
+// 32 experts several warps share one, each with a part of the tokens).
 __device__ void sum_slice(const float* __restrict__ scores, const int32_t* __restrict__ idx,
                           const uint8_t* __restrict__ mask, int T, int E, int k, uint32_t t0,
                           uint32_t t1, Partial& out) {
   __shared__ float part[kWarps][2];  // a warp's experts: at most two
   __shared__ int32_t count_s[kMaxE];
-  __shared__ int32_t tokens_s;
+  __shared__ uint32_t on_s[kWarps];  // bit l of word w: token 32 w + l counts
+  __shared__ int32_t tokens_s[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < kMaxE) count_s[tid] = 0;
-  if (tid == kMaxE) tokens_s = 0;
   // Experts of a round of warps (a power of two), and warps to an expert.
   const int wide = E > 16 ? 32 : E > 8 ? 16 : E > 4 ? 8 : E > 2 ? 4 : E;
   const int share = kWarps / wide, e0 = warp % wide, q = warp / wide;
-  // The first tokens' experts are asked for before the scores, and counted
-  // after them.
-  auto load = [&](uint32_t t, int (&sel)[kMaxK]) {
-    const bool counted = t < t1 && (!mask || mask[t]);
+  float s[2] = {0.f, 0.f};
+  int32_t tokens = 0;
+  for (uint32_t c0 = t0; c0 < t1; c0 += kThreads) {
+    const uint32_t c1 = t1 - c0 < kThreads ? t1 : c0 + kThreads, tok = c0 + tid;
+    const bool counted = tok < c1 && (!mask || mask[tok]);
+    int sel[kMaxK];
 #pragma unroll
     for (int j = 0; j < kMaxK; ++j)
-      sel[j] = t < t1 && j < k ? __ldg(idx + static_cast<int64_t>(t) * k + j) : -1;
-    return counted;
-  };
-  int sel[kMaxK];
-  uint32_t tok = t0 + tid;
-  bool counted = load(tok, sel);
-  float s[2] = {0.f, 0.f};
-  for (uint32_t t = t0 + q * 32 * kBatch + lane; t < t1; t += share * 32 * kBatch) {
-    float v[2][kBatch];
-    uint32_t on = 0;
+      sel[j] = tok < c1 && j < k ? __ldg(idx + static_cast<int64_t>(tok) * k + j) : -1;
+    bool first = true;
+    for (uint32_t t = c0 + q * 32 * kBatch; t < c1 || first; t += share * 32 * kBatch) {
+      float v[2][kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const uint32_t at = t + 32 * i;
-      const bool in = at < t1;
-      if (in && (!mask || mask[at])) on |= 1u << i;
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t at = t + 32 * i + lane;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int e = e0 + h * wide;
-        v[h][i] = in && e < E ? __ldg(scores + static_cast<int64_t>(e) * T + at) : 0.f;
+        for (int h = 0; h < 2; ++h) {
+          const int e = e0 + h * wide;
+          v[h][i] = at < c1 && e < E ? __ldg(scores + static_cast<int64_t>(e) * T + at) : 0.f;
+        }
+      }
+      if (first) {
+        // Every load of the first batch is on its way: now the mask's words.
+        const unsigned word = __ballot_sync(0xffffffffu, counted);
+        if (lane == 0) on_s[warp] = word;
+        tokens += __popc(word);
+        first = false;
+        __syncthreads();
+      }
+      // A token that does not count may hold anything: left out, not times 0.
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t w = (t - c0) / 32 + i;
+        const bool on = w < kWarps && (on_s[w % kWarps] >> lane & 1u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[h] += on ? v[h][i] : 0.f;
       }
     }
-    // A token that does not count may hold anything: left out, not times 0.
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) s[h] += on >> i & 1u ? v[h][i] : 0.f;
-  }
-  __syncthreads();  // the counters are zero
-  for (;;) {
-    const unsigned any = __ballot_sync(0xffffffffu, counted);
-    if (lane == 0 && any) atomicAdd(&tokens_s, __popc(any));
 #pragma unroll
     for (int j = 0; j < kMaxK; ++j)
       if (counted && sel[j] >= 0 && sel[j] < E) atomicAdd(&count_s[sel[j]], 1);
-    tok += kThreads;
-    if (tok - lane >= t1) break;
-    counted = load(tok, sel);
+    if (t1 - c0 > kThreads) __syncthreads();  // before the next words
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -116,6 +119,7 @@ __device__ void sum_slice(const float* __restrict__ scores, const int32_t* __res
     for (int o = 16; o > 0; o >>= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], o);
     if (lane == 0) part[warp][h] = s[h];
   }
+  if (lane == 0) tokens_s[warp] = tokens;
   __syncthreads();
   if (tid < kMaxE) {
     float total = 0.f;
@@ -123,8 +127,12 @@ __device__ void sum_slice(const float* __restrict__ scores, const int32_t* __res
       for (int i = 0; i < share; ++i) total += part[tid % wide + i * wide][tid / wide];
     out.sum[tid] = total;
     out.count[tid] = count_s[tid];
+  } else if (warp == kMaxE / 32) {
+    int32_t n = tokens_s[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0) out.tokens = n;
   }
-  if (tid == kMaxE) out.tokens = tokens_s;
 }
 
 // The loss from the totals, by the first two warps (thread e: expert e).
