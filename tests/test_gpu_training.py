@@ -140,6 +140,13 @@ ROUTE = [
     (700, 320, 63, 7, "fp32", "softmax_topk", 1.0, True, True, "some", True),
     # ranges of many tiles, three blocks of terms
     (6000, 2056, 64, 8, "bf16", "softmax_topk", 1.0, True, True, "some", True),
+    # one expert: nothing to learn, zeros
+    (70, 72, 1, 1, "bf16", "topk_softmax", 1.0, True, True, "some", True),
+    (70, 72, 1, 1, "fp32", "softmax_topk", 1.0, True, True, None, False),
+    # more column blocks than SMs: a range of 4, 5 and 9 tiles each
+    (512, 19208, 8, 2, "bf16", "topk_softmax", 1.0, True, True, None, True),
+    (640, 19208, 64, 2, "bf16", "softmax_topk", 1.0, True, True, "some", False),
+    (1025, 19208, 24, 2, "bf16", "topk_softmax", 1.0, True, True, "some", True),
     # a padded batch whose tail is all padding (whole tiles of it)
     (1500, 264, 8, 2, "bf16", "topk_softmax", 1.0, True, True, "tail", True),
 ]
