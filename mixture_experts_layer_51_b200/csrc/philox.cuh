@@ -56,15 +56,4 @@ __host__ __device__ __forceinline__ bool dropout_kept(const uint32_t (&w)[4], in
   return high >= threshold << 16;
 }
 
-// All eight: bit i is set where element 8 n + i is kept.
-__host__ __device__ __forceinline__ uint32_t dropout_keep8(uint64_t n, uint64_t offset,
-                                                           uint64_t seed, uint32_t threshold) {
-  uint32_t w[4];
-  philox4x32_10(n, offset, philox_keys(seed), w);
-  uint32_t keep = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) keep |= (dropout_kept(w, i, threshold) ? 1u : 0u) << i;
-  return keep;
-}
-
 }  // namespace moe

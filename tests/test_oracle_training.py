@@ -36,7 +36,12 @@ def test_the_kernels_generator_on_the_host(tmp_path):
 #include "philox.cuh"
 int main(int, char** v) {
   const uint64_t n = strtoull(v[1], 0, 0), off = strtoull(v[2], 0, 0), seed = strtoull(v[3], 0, 0);
-  for (int i = 0; i < 64; ++i) printf("%u ", moe::dropout_keep8(n + i, off, seed, atoi(v[4])));
+  for (int i = 0; i < 64; ++i) {
+    uint32_t w[4], keep = 0;
+    moe::philox4x32_10(n + i, off, moe::philox_keys(seed), w);
+    for (int j = 0; j < 8; ++j) keep |= (moe::dropout_kept(w, j, atoi(v[4])) ? 1u : 0u) << j;
+    printf("%u ", keep);
+  }
 }
 """)
     exe = tmp_path / "p"
