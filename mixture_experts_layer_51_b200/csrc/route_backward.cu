@@ -9,7 +9,8 @@
 //   balance loss:        dz_e += dL coef (E / N) p_e (f_e - sum_i f_i p_i)
 //   dx = dx_acc + dz W_g^T,   dW_g = x^T dz,   dbias = sum_t dz
 //
-// Two launches.  (1) dz for every token, and its column sums per block of
+// Small batches go to route_backward_small.cu in one launch; the others take
+// two launches.  (1) dz for every token, and its column sums per block of
 // tokens.  (2) Both products in one pass over x: a CTA owns a block of
 // columns and a range of tokens, so each x element is read once, each dx
 // element written once, and dW_g of the block stays on the chip until the
@@ -492,6 +493,8 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& a, moe_dtype dtype, c
                        p.ranges,
                        a.d,
                        a.E};
+  if (route_backward_is_small(a.T, a.d, a.E))
+    return launch_route_backward_small(a, dtype, sums.err, s);
   const bool tc = dtype == MOE_BF16;
   auto dz = [&](auto kern) {
     return launch_kernel(kern, dim3(p.blocks), dim3(kDzThreads), 0, s, 1, true, a, p.EP,

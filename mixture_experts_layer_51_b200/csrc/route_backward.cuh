@@ -107,6 +107,11 @@ __device__ __forceinline__ void sum_ranges(const RouteSums& s, int c0, int cols,
 
 cudaError_t launch_route_products_tc(const RouteBackwardArgs& a, const RouteBackwardPlan& p,
                                      const RouteSums& sums, cudaStream_t s);
+// Small batches in one launch (route_backward_small.cu).
+constexpr int kRbSmallTokens = 256;
+bool route_backward_is_small(int T, int d, int E);
+cudaError_t launch_route_backward_small(const RouteBackwardArgs& a, moe_dtype dtype, int32_t* err,
+                                        cudaStream_t s);
 constexpr int kRbTcCols = 128;   // columns and tokens of one tile
 constexpr int kRbTcTokens = 128;
 constexpr int kRbPartBytes = 32768;  // a column block's dW_g of one range, three blocks of terms

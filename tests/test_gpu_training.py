@@ -140,6 +140,16 @@ ROUTE = [
     (700, 320, 63, 7, "fp32", "softmax_topk", 1.0, True, True, "some", True),
     # ranges of many tiles, three blocks of terms
     (6000, 2056, 64, 8, "bf16", "softmax_topk", 1.0, True, True, "some", True),
+    # around the sizes up to which one launch does it all
+    (256, 264, 8, 2, "bf16", "softmax_topk", 1.0, True, True, "some", True),
+    (256, 264, 16, 4, "fp32", "topk_softmax", 2.0, True, True, "some", True),
+    (257, 264, 16, 4, "fp32", "topk_softmax", 2.0, True, True, "some", True),
+    (255, 40, 9, 8, "bf16", "topk_softmax", 1.0, True, True, None, False),
+    (128, 4736, 32, 2, "bf16", "softmax_topk", 1.0, True, True, "bytes", True),
+    (129, 4736, 32, 2, "bf16", "softmax_topk", 1.0, True, True, "bytes", True),
+    (64, 104, 64, 8, "bf16", "softmax_topk", 1.0, True, True, "some", False),
+    (64, 104, 57, 8, "fp32", "topk_softmax", 1.0, True, True, "tail", True),
+    (2, 4744, 3, 1, "bf16", "softmax_topk", 1.0, True, True, None, True),
     # one expert: nothing to learn, zeros
     (70, 72, 1, 1, "bf16", "topk_softmax", 1.0, True, True, "some", True),
     (70, 72, 1, 1, "fp32", "softmax_topk", 1.0, True, True, None, False),
@@ -242,8 +252,8 @@ def test_route_backward(case):
 
 @pytest.mark.parametrize("outputs", [("dx",), ("dWg",), ("dbias",), ("dx", "dbias"),
                                      ("dWg", "dbias")])
-@pytest.mark.parametrize("case", [ROUTE[3], ROUTE[12], ROUTE[13]],
-                         ids=["bf16", "bf16-wide", "fp32"])
+@pytest.mark.parametrize("case", [ROUTE[3], ROUTE[4], ROUTE[12], ROUTE[13]],
+                         ids=["bf16-small", "fp32-small", "bf16", "fp32"])
 def test_route_backward_of_some_outputs(case, outputs):
     """Asking for less gives the same bits of what is asked for."""
     a = _route_case(*case)
@@ -254,7 +264,8 @@ def test_route_backward_of_some_outputs(case, outputs):
         assert torch.equal(got[name], want[name]), name
 
 
-@pytest.mark.parametrize("case", [ROUTE[4], ROUTE[9], ROUTE[15]], ids=["fp32", "bf16", "bf16-wide"])
+@pytest.mark.parametrize("case", [ROUTE[4], ROUTE[6], ROUTE[9], ROUTE[13], ROUTE[15]],
+                         ids=["fp32-small", "bf16-small", "bf16", "fp32", "bf16-wide"])
 def test_route_backward_never_looks_at_padding(case):
     """NaN in a padding token's x, scores, gates and gate gradients reaches
     nothing; its dx row is its dx_acc, or zero."""
@@ -276,7 +287,8 @@ def test_route_backward_never_looks_at_padding(case):
     assert torch.equal(got["dx"][off], rows)
 
 
-@pytest.mark.parametrize("case", [ROUTE[3], ROUTE[4], ROUTE[16]], ids=["bf16", "fp32", "wide"])
+@pytest.mark.parametrize("case", [ROUTE[3], ROUTE[4], ROUTE[13], ROUTE[16]],
+                         ids=["bf16-small", "fp32-small", "fp32", "bf16"])
 def test_route_backward_adds_in_place(case):
     a = _route_case(*case)
     want = M.moe_route_backward(**a)["dx"]
@@ -287,7 +299,7 @@ def test_route_backward_adds_in_place(case):
 
 def test_route_backward_stays_inside_its_buffers():
     """Guard rows around every output and the workspace keep their bytes."""
-    for case in (ROUTE[1], ROUTE[2], ROUTE[6], ROUTE[8], ROUTE[9], ROUTE[15]):
+    for case in (ROUTE[1], ROUTE[2], ROUTE[6], ROUTE[8], ROUTE[9], ROUTE[13], ROUTE[15]):
         a = _route_case(*case)
         T, d = a["x"].shape
         E = a["Wg"].shape[1]
