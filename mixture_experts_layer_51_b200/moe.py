@@ -10,6 +10,7 @@ fallback: if libmoe.so is missing or was not built, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -743,12 +744,19 @@ def _cuda_device(t, name):
 # around it, which takes as long as a kernel launch.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+@functools.lru_cache(maxsize=32)
+def _route_options(gating, gate_scale):
+    """The options of a gate formula and scale (the library only reads them)."""
+    return ctypes.byref(_options(gating, gate_scale))
 
 
 def _launch(fn, where, dev, stream, *args):
     """fn(*args, stream) with ``dev`` current (its own stream if none is given)."""
     s = stream.cuda_stream if stream is not None else _raw_stream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         status = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -844,7 +852,6 @@ def moe_route_backward(x, Wg, idx, gate=None, dgate=None, scores=None, counts=No
         raise ValueError(f"outputs {outputs}: dx, dWg and dbias, each at most once")
     ws = _workspace(ws, 0 if ws is not None else
                     moe_route_backward_workspace_bytes(T, d, E, dt), dev, stream)
-    opt = _options(gating, gate_scale)
     _launch(lib().moe_route_backward, "moe_route_backward", dev, stream,
             _tensor(x, "x", dt, (T, d), dev), _tensor(Wg, "Wg", dt, (d, E), dev),
             _tensor(scores, "scores", f32, (E, T), dev), _tensor(idx, "idx", i32, (T, k), dev),
@@ -852,7 +859,8 @@ def moe_route_backward(x, Wg, idx, gate=None, dgate=None, scores=None, counts=No
             _tensor(counts, "counts", i32, (E,), dev), _tensor(tokens, "tokens", i32, (1,), dev),
             _tensor(dloss, "dloss", f32, (1,), dev), coef,
             _mask(mask, T, dev),
-            _tensor(dx_acc, "dx_acc", dt, (T, d), dev), T, d, E, k, code, ctypes.byref(opt),
+            _tensor(dx_acc, "dx_acc", dt, (T, d), dev), T, d, E, k, code,
+            _route_options(gating, gate_scale),
             _tensor(dx, "dx", dt, (T, d), dev), _tensor(dWg, "dWg", f32, (d, E), dev),
             _tensor(dbias, "dbias", f32, (E,), dev), ws.data_ptr(),
             ws.numel() * ws.element_size())
