@@ -10,16 +10,14 @@
 //   dx = dx_acc + dz W_g^T,   dW_g = x^T dz,   dbias = sum_t dz
 //
 // Small batches go to route_backward_small.cu in one launch; the others take
-// two launches.  (1) dz for every token, and its column sums per block of
+// two launches or three.  (1) dz for every token, and its column sums per block of
 // tokens.  (2) Both products in one pass over x: a CTA owns a block of
 // columns and a range of tokens, so each x element is read once, each dx
 // element written once, and dW_g of the block stays on the chip until the
 // range is done (bf16: tensor cores, route_backward_tc.cu; fp32: FMA, here).
 // The last range of a column block to finish adds all of the block's ranges
-// in order, and one warp an expert the dz blocks' column sums, so no sum
-// depends on scheduling (no floating-point atomics).  Adding them in a third
-// launch took as long on the GPU (56.8 and 56.0 us on the fine-grained shape)
-// and 2 us more of the host.
+// in order, or a third launch does, and one warp an expert adds the dz blocks'
+// column sums: no sum depends on scheduling (no floating-point atomics).
 //
 // dz is a launch of its own because every column block needs it: 5.6 MB of
 // scores and gates in, 128 to 384 bytes a token out (bf16 terms), 7 us for
@@ -55,6 +53,17 @@ int pick_ranges(int cols, int tiles, int per_sm) {
   return best;
 }
 
+// The ranges of dW_g are added by the last CTA of a column block, or by a
+// launch over all SMs.  The launch is quicker on the GPU from about five
+// ranges on (16384 x 2048, 64 experts, 9 ranges: 39.8 us for the pass against
+// 42.1; 4096 x 1024 fp32, 16 ranges: 15.0 against 18.1; 16384 x 64, 64
+// experts, 128 ranges: 13.7 against 51; at four ranges both take 39.8 us), but
+// costs the host 2.3 us.  So passes that the host bounds anyway (x of less
+// than 8 MB) do without, as long as one CTA has no more than 20 to add.
+constexpr int kFewRanges = 4;
+constexpr int kPassingRanges = 20;
+constexpr int64_t kSummingLaunchBytes = 8 << 20;
+
 RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   RouteBackwardPlan p{};
   const bool tc = dtype == MOE_BF16;
@@ -64,6 +73,9 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   p.cols = (d + cols - 1) / cols;
   p.tiles = (T + tile - 1) / tile;
   p.ranges = T > 0 ? pick_ranges(p.cols, p.tiles, tc ? 1 : 2) : 0;
+  p.many = p.ranges > kPassingRanges ||
+           (p.ranges > kFewRanges &&
+            static_cast<int64_t>(T) * d * (tc ? 2 : 4) >= kSummingLaunchBytes);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -75,7 +87,7 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   const size_t row = tc ? 128 * dz_terms(E).blocks : sizeof(float) * p.EP;
   p.dz = take(row * T);
   p.bias = take(sizeof(float) * kMaxE * p.blocks);
-  p.dw = take(tc && dz_terms(E).blocks == 3
+  p.dw = take(tc && dz_terms(E).blocks == 3 && !p.many
                   ? static_cast<size_t>(kRbPartBytes) * p.cols * p.ranges
                   : sizeof(float) * d * E * p.ranges);
   p.total = at;
@@ -433,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (e >= a.E) e -= a.E, ++c;
     }
   }
+  if (sums.many) return;
   __threadfence();
   __syncthreads();
   if (tid == 0)
@@ -441,6 +454,30 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (!sm.last) return;
   __threadfence();
   sum_ranges(sums, c0, cols, tid, kThreads, sm.scratch, [] { __syncthreads(); });
+}
+
+// dW_g from many ranges' parts: 32 pieces of 16 bytes a CTA, each by eight
+// warps that share out the ranges and are added up in order.
+__global__ void __launch_bounds__(kThreads) route_finish_kernel(const RouteSums s) {
+  constexpr int G = kThreads / 32;
+  __shared__ float4 part[G][32];
+  const int lane = threadIdx.x % 32, g = threadIdx.x / 32;
+  const int64_t n = static_cast<int64_t>(s.d) * s.E / 4;  // columns come in eights
+  const int64_t v = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  pdl_wait();
+  pdl_trigger();
+  const float4* from = reinterpret_cast<const float4*>(s.dw) + v;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& b) { sum.x += b.x, sum.y += b.y, sum.z += b.z, sum.w += b.w; };
+  if (v < n)
+#pragma unroll 8
+    for (int r = g; r < s.ranges; r += G) add(from[r * n]);
+  part[g][lane] = sum;
+  __syncthreads();
+  if (g > 0 || v >= n) return;
+  for (int i = 1; i < G; ++i) add(part[i][lane]);
+  if (*s.err != 0) sum.x = sum.y = sum.z = sum.w = __int_as_float(0x7fc00000);
+  reinterpret_cast<float4*>(s.dWg)[v] = sum;
 }
 
 // The bias alone: one warp an expert.
@@ -492,7 +529,8 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& a, moe_dtype dtype, c
                        p.blocks,
                        p.ranges,
                        a.d,
-                       a.E};
+                       a.E,
+                       p.many};
   if (route_backward_is_small(a.T, a.d, a.E))
     return launch_route_backward_small(a, dtype, sums.err, s);
   const bool tc = dtype == MOE_BF16;
@@ -501,15 +539,19 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& a, moe_dtype dtype, c
                          dz_terms(a.E), static_cast<void*>(ws + p.dz), bias, sums.err,
                          sums.tickets, p.cols);
   };
-  const cudaError_t err =
+  cudaError_t err =
       a.E <= 8    ? (tc ? dz(route_dz_kernel<true, 1>) : dz(route_dz_kernel<false, 1>))
       : a.E <= 16 ? (tc ? dz(route_dz_kernel<true, 2>) : dz(route_dz_kernel<false, 2>))
       : a.E <= 32 ? (tc ? dz(route_dz_kernel<true, 4>) : dz(route_dz_kernel<false, 4>))
                   : (tc ? dz(route_dz_kernel<true, 8>) : dz(route_dz_kernel<false, 8>));
   if (err != cudaSuccess) return err;
   if (!a.dx && !a.dWg) return launch_kernel(route_bias_kernel, dim3(a.E), dim3(32), 0, s, 1, true, sums);
-  return tc ? launch_route_products_tc(a, p, sums, s)
-            : launch_products(a, p, sums, reinterpret_cast<const float*>(ws + p.dz), s);
+  err = tc ? launch_route_products_tc(a, p, sums, s)
+           : launch_products(a, p, sums, reinterpret_cast<const float*>(ws + p.dz), s);
+  if (err != cudaSuccess || !a.dWg || !sums.many) return err;
+  const int64_t pieces = static_cast<int64_t>(a.d) * a.E / 4;
+  return launch_kernel(route_finish_kernel, dim3(static_cast<unsigned>((pieces + 31) / 32)),
+                       dim3(kThreads), 0, s, 1, true, sums);
 }
 
 }  // namespace moe

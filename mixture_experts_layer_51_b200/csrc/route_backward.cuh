@@ -29,6 +29,7 @@ struct RouteBackwardPlan {
   int cols;    // column blocks of the products
   int ranges;  // token ranges of the products
   int tiles;   // token tiles, shared out over the ranges
+  bool many;   // a launch of its own adds the ranges of dW_g
   size_t err, tickets, dz, bias, dw, total;  // byte offsets
 };
 
@@ -44,6 +45,9 @@ struct RouteSums {
   float* dWg;         // null: not wanted
   float* dbias;
   int blocks, ranges, d, E;
+  // The ranges are added by a launch of their own, and the parts are
+  // [ranges, d, E] whatever the terms.
+  int many;
 };
 
 // dbias of expert e by one warp: lanes over the blocks, then a tree.

@@ -488,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // fewer, the terms are added first.
       float4* mine = reinterpret_cast<float4*>(p.sums.dw) + block * (kPartBytes / 16) + et;
       const int64_t plane = static_cast<int64_t>(p.cols) * (kPartBytes / 16);
-      if (ok && NB == 3) {
+      const bool as_held = NB == 3 && !p.sums.many;
+      if (ok && as_held) {
 #pragma unroll
         for (int j = 0; j < ACC / 4; ++j)
           mine[range * plane + j * kEpilogue] =
@@ -497,12 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* out = p.sums.dw + (static_cast<int64_t>(range) * p.d + c0) * p.E;
         through_ring([&](int i, float v) { out[i] = v; });
       }
-      __threadfence();
-      epilogue_sync();
-      if (et == 0)
-        c.last = atomicAdd(p.sums.tickets + block, 1u) + 1 == static_cast<uint32_t>(p.ranges);
-      epilogue_sync();
-      if (c.last) {
+      bool last = false;
+      if (!p.sums.many) {
+        __threadfence();
+        epilogue_sync();
+        if (et == 0)
+          c.last = atomicAdd(p.sums.tickets + block, 1u) + 1 == static_cast<uint32_t>(p.ranges);
+        epilogue_sync();
+        last = c.last;
+      }
+      if (last) {
         __threadfence();
         if (NB == 3) {
           const bool failed = *static_cast<volatile int32_t*>(p.sums.err) != 0;

@@ -140,6 +140,11 @@ ROUTE = [
     (700, 320, 63, 7, "fp32", "softmax_topk", 1.0, True, True, "some", True),
     # ranges of many tiles, three blocks of terms
     (6000, 2056, 64, 8, "bf16", "softmax_topk", 1.0, True, True, "some", True),
+    # many ranges of few columns, and a large pass, whose ranges a launch adds
+    (20000, 64, 44, 2, "bf16", "topk_softmax", 1.0, True, True, "some", False),
+    (20000, 64, 8, 2, "fp32", "softmax_topk", 1.0, True, True, "some", True),
+    (9000, 520, 30, 2, "bf16", "topk_softmax", 1.0, False, True, None, False),
+    (5000, 1160, 6, 2, "bf16", "topk_softmax", 1.0, False, True, None, True),
     # around the sizes up to which one launch does it all
     (256, 264, 8, 2, "bf16", "softmax_topk", 1.0, True, True, "some", True),
     (256, 264, 16, 4, "fp32", "topk_softmax", 2.0, True, True, "some", True),
@@ -252,8 +257,8 @@ def test_route_backward(case):
 
 @pytest.mark.parametrize("outputs", [("dx",), ("dWg",), ("dbias",), ("dx", "dbias"),
                                      ("dWg", "dbias")])
-@pytest.mark.parametrize("case", [ROUTE[3], ROUTE[4], ROUTE[12], ROUTE[13]],
-                         ids=["bf16-small", "fp32-small", "bf16", "fp32"])
+@pytest.mark.parametrize("case", [ROUTE[3], ROUTE[4], ROUTE[12], ROUTE[13], ROUTE[14]],
+                         ids=["bf16-small", "fp32-small", "bf16", "fp32", "bf16-many"])
 def test_route_backward_of_some_outputs(case, outputs):
     """Asking for less gives the same bits of what is asked for."""
     a = _route_case(*case)
