@@ -10,16 +10,16 @@
 // never stored.  A dropped element is left out, not multiplied by zero, so
 // what stands there (infinities, NaN) reaches neither y nor a gradient.
 //
-// One token's row is owned by whole warps of one CTA, so the k gate gradients
+// One token's row is owned by the lanes of one CTA, so the k gate gradients
 // are a fixed-order sum and nothing is atomic; every permuted row belongs to
 // one (token, slot), so the scatter of d_o writes each row once.
 //
 // Bound by HBM: the kept rows of o, y or dy, the residual, d_o, each once.
 // Measured on one B200 (floors at 6.56 TB/s in brackets), p = 0.1, bf16:
-// forward with residual 8192 x 4096 top-2 42.4 us (40.9), 16384 x 2048 top-8
-// 98.8 us (102.4); backward 8192 x 4096 top-2 54.1 us (51.2; 53.2 without
-// dropout, so the generator hides behind the copies), 16384 x 2048 top-8
-// 180 us (174).  What made the difference: all loads of a sweep before any
+// forward with residual 8192 x 4096 top-2 42.4 us (40.9), top-4 60.6 (61.4),
+// 16384 x 2048 top-8 98.5 us (102.4); backward 8192 x 4096 top-2 54.2 us (51.2;
+// 53.2 without dropout, so the generator hides behind the copies), top-4 95.9
+// (92.1), 16384 x 2048 top-8 180 us (174).  What made the difference: all loads of a sweep before any
 // arithmetic (156 -> 106 us on the top-8 forward), plain instead of
 // evict-first loads (192 -> 185 us on the top-8 backward), and four sweeps a
 // warp (57.5 -> 55.8 us on 8192 x 4096).  More resident warps through fewer
@@ -106,54 +106,61 @@ __device__ __forceinline__ void keep_masks(const uint32_t (&w)[4], uint32_t thre
   }
 }
 
-// Warps of a CTA sharing one token's row (1, 2, 4 or 8): this warp's token,
-// and which of the token's warps it is.
+// A token's row belongs to L lanes of a warp (8 or 32), or of each of
+// 1 << warp_bits warps of a CTA (L = 32 only): this thread's token, which of
+// the token's warps it is in, and its lane there.
 struct Place {
   int64_t t;
-  int part;
+  int part, lane;
 };
-__device__ __forceinline__ Place place(int wpt) {
-  const int warp = threadIdx.x >> 5;
-  return {static_cast<int64_t>(blockIdx.x) * (kCdWarps / wpt) + warp / wpt, warp % wpt};
+__host__ __device__ constexpr int tokens_per_cta(int L, int warp_bits) {
+  return kCdWarps * 32 / L >> warp_bits;
+}
+template <int L>
+__device__ __forceinline__ Place place(int warp_bits) {
+  const int thread = threadIdx.x, group = thread / L;
+  return {static_cast<int64_t>(blockIdx.x) * tokens_per_cta(L, warp_bits) + (group >> warp_bits),
+          group & ((1 << warp_bits) - 1), thread % L};
 }
 
-// The token's rows and gates, in every lane (row -1: no such slot).
-template <int KJ>
-__device__ __forceinline__ void slots(const int32_t* pos, const float* gate, int64_t t, int k,
-                                      int (&row)[KJ], float (&g)[KJ]) {
-  const int lane = threadIdx.x & 31;
-  const int pl = lane < k ? pos[t * k + lane] : -1;
-  const float gl = lane < k ? gate[t * k + lane] : 0.f;
+// The token's rows and gates, in every lane of it (row -1: no such slot, as
+// for tokens past the last).  Whole warps call this.
+template <int KJ, int L>
+__device__ __forceinline__ void slots(const int32_t* pos, const float* gate, const Place& at,
+                                      int T, int k, int (&row)[KJ], float (&g)[KJ]) {
+  const bool in = at.t < T && at.lane < k;
+  const int pl = in ? pos[at.t * k + at.lane] : -1;
+  const float gl = in ? gate[at.t * k + at.lane] : 0.f;
 #pragma unroll
   for (int j = 0; j < KJ; ++j) {
-    row[j] = __shfl_sync(0xffffffffu, pl, j);
-    g[j] = __shfl_sync(0xffffffffu, gl, j);
+    row[j] = __shfl_sync(0xffffffffu, pl, j, L);
+    g[j] = __shfl_sync(0xffffffffu, gl, j, L);
   }
 }
 
-// KJ = slots this instantiation handles (2 for k <= 2, else kMaxK); CH =
+// KJ = slots this instantiation handles (2, 4 or 8, the least that k fits); CH =
 // 8-element chunks of each row per lane and iteration: every load of an
 // iteration is issued before any arithmetic (the generator's, too, runs while
 // they are on their way).
-template <bool BF16, int KJ, int CH>
+template <bool BF16, int KJ, int CH, int L>
 __global__ void __launch_bounds__(kCdWarps * 32)
     combine_dropout_kernel(const void* __restrict__ o, const int32_t* __restrict__ pos,
                            const float* __restrict__ gate, const void* residual,
                            const uint64_t* __restrict__ rng, uint32_t threshold, float scale,
-                           int T, int d, int k, int wpt, void* y) {
+                           int T, int d, int k, int warp_bits, void* y) {
   pdl_wait();
   pdl_trigger();
   constexpr uint32_t B = Chunk<BF16>::kBytes;
-  const Place at = place(wpt);
-  if (at.t >= T) return;
+  const Place at = place<L>(warp_bits);
   const int64_t t = at.t;
-  const uint32_t n8 = d / 8, lane = threadIdx.x & 31;
+  const uint32_t n8 = d / 8;
   uint64_t seed = 0, offset = 0;
   if (threshold) seed = rng[0], offset = rng[1];
   int row[KJ];
   float g[KJ];
   const char* from[KJ];
-  slots<KJ>(pos, gate, t, k, row, g);
+  slots<KJ, L>(pos, gate, at, T, k, row, g);
+  if (t >= T) return;
 #pragma unroll
   for (int j = 0; j < KJ; ++j) {
     g[j] *= scale;
@@ -162,30 +169,30 @@ __global__ void __launch_bounds__(kCdWarps * 32)
   const char* rest = static_cast<const char*>(residual) + t * n8 * B;
   char* to = static_cast<char*>(y) + t * n8 * B;
   const PhiloxKeys keys = philox_keys(seed);
-  for (uint32_t c0 = at.part * 32 * CH + lane; c0 < n8; c0 += wpt * 32 * CH) {
+  for (uint32_t c0 = at.part * L * CH + at.lane; c0 < n8; c0 += L * CH << warp_bits) {
     const uint64_t at_c = static_cast<uint64_t>(c0) * B;
     Chunk<BF16> v[KJ][CH], res[CH];
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
-      const bool in = c0 + h * 32 < n8;
+      const bool in = c0 + h * L < n8;
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
         if (row[j] >= 0 && in)
-          v[j][h].load(from[j] + at_c + h * 32 * B);
+          v[j][h].load(from[j] + at_c + h * L * B);
         else
           v[j][h].zero();
       }
       if (residual && in)
-        res[h].load(rest + at_c + h * 32 * B);
+        res[h].load(rest + at_c + h * L * B);
       else
         res[h].zero();
     }
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
-      if (c0 + h * 32 >= n8) break;
+      if (c0 + h * L >= n8) break;
       float acc[8] = {}, f[8];
       uint32_t w[4];
-      if (threshold) philox4x32_10(t * n8 + c0 + h * 32, offset, keys, w);
+      if (threshold) philox4x32_10(t * n8 + c0 + h * L, offset, keys, w);
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
         if (row[j] < 0) continue;  // absent slots add nothing
@@ -202,17 +209,18 @@ __global__ void __launch_bounds__(kCdWarps * 32)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] += f[i];
       }
-      Chunk<BF16>::store(to + at_c + h * 32 * B, acc);
+      Chunk<BF16>::store(to + at_c + h * L * B, acc);
     }
   }
 }
 
-// Adds `v` over the 32 lanes: afterwards lane l holds in the result the total
-// of v[l / (32 / N) % N], each added in an order that is always the same.
-template <int N>
+// Adds `v` over each group of L lanes (at least N): afterwards lane l of a
+// group holds the total of v[l / (L / N)], each added in an order that is
+// always the same.
+template <int N, int L>
 __device__ __forceinline__ float reduce_lanes(float (&v)[N]) {
   const int lane = threadIdx.x & 31;
-  int s = 16;
+  int s = L / 2;
 #pragma unroll
   for (int n = N / 2; n > 0; n /= 2, s /= 2) {
     // The upper half of the lanes keeps the upper half of the values.
@@ -229,31 +237,28 @@ __device__ __forceinline__ float reduce_lanes(float (&v)[N]) {
   return v[0];
 }
 
-template <bool BF16, int KJ, int CH>
+template <bool BF16, int KJ, int CH, int L>
 __global__ void __launch_bounds__(kCdWarps * 32)
     combine_dropout_backward_kernel(const void* __restrict__ dy, const void* __restrict__ o,
                                     const int32_t* __restrict__ pos,
                                     const float* __restrict__ gate,
                                     const uint64_t* __restrict__ rng, uint32_t threshold,
-                                    float scale, int T, int d, int k, int wpt,
+                                    float scale, int T, int d, int k, int warp_bits,
                                     void* __restrict__ d_o, float* __restrict__ dgate) {
   __shared__ float part[kCdWarps][KJ];
   pdl_wait();
   pdl_trigger();
-  const Place at = place(wpt);
+  const Place at = place<L>(warp_bits);
   constexpr uint32_t B = Chunk<BF16>::kBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = at.lane;
   const int64_t t = at.t;
   const uint32_t n8 = d / 8;
-  float dot[KJ] = {};
+  float dot[KJ] = {}, g[KJ];
   int row[KJ];
-#pragma unroll
-  for (int j = 0; j < KJ; ++j) row[j] = -1;
-  if (at.t < T) {
-    float g[KJ];
-    uint64_t seed = 0, offset = 0;
-    if (threshold) seed = rng[0], offset = rng[1];
-    slots<KJ>(pos, gate, t, k, row, g);
+  uint64_t seed = 0, offset = 0;
+  if (threshold) seed = rng[0], offset = rng[1];
+  slots<KJ, L>(pos, gate, at, T, k, row, g);
+  if (t < T) {
     const char* from[KJ];
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
@@ -263,26 +268,26 @@ __global__ void __launch_bounds__(kCdWarps * 32)
     const char* up_row = static_cast<const char*>(dy) + t * n8 * B;
     char* to = static_cast<char*>(d_o);
     const PhiloxKeys keys = philox_keys(seed);
-    for (uint32_t c0 = at.part * 32 * CH + lane; c0 < n8; c0 += wpt * 32 * CH) {
+    for (uint32_t c0 = at.part * L * CH + at.lane; c0 < n8; c0 += L * CH << warp_bits) {
       const uint64_t at_c = static_cast<uint64_t>(c0) * B;
       Chunk<BF16> v[KJ][CH], up[CH];
 #pragma unroll
       for (int h = 0; h < CH; ++h) {
-        if (c0 + h * 32 >= n8) break;
-        up[h].load(up_row + at_c + h * 32 * B);
+        if (c0 + h * L >= n8) break;
+        up[h].load(up_row + at_c + h * L * B);
 #pragma unroll
         for (int j = 0; j < KJ; ++j)
-          if (row[j] >= 0) v[j][h].load(from[j] + at_c + h * 32 * B);
+          if (row[j] >= 0) v[j][h].load(from[j] + at_c + h * L * B);
       }
 #pragma unroll
       for (int h = 0; h < CH; ++h) {
-        if (c0 + h * 32 >= n8) break;
+        if (c0 + h * L >= n8) break;
         // Dropped elements become zero in dy and in o (what o holds there is
         // left out: 0 times it need not be 0).
         uint32_t m[4];
         if (threshold) {
           uint32_t w[4];
-          philox4x32_10(t * n8 + c0 + h * 32, offset, keys, w);
+          philox4x32_10(t * n8 + c0 + h * L, offset, keys, w);
           keep_masks(w, threshold, m);
           up[h].mask(m);
         }
@@ -299,70 +304,90 @@ __global__ void __launch_bounds__(kCdWarps * 32)
             dot[j] = fmaf(a[i], f[i], dot[j]);
             f[i] = g[j] * a[i];  // g carries the scale
           }
-          Chunk<BF16>::store(to + (from[j] - static_cast<const char*>(o)) + at_c + h * 32 * B, f);
+          Chunk<BF16>::store(to + (from[j] - static_cast<const char*>(o)) + at_c + h * L * B, f);
         }
       }
     }
   }
   // The row's dot products: over the lanes, then over the warps that share it.
-  const float sum = scale * reduce_lanes<KJ>(dot);
-  constexpr int W = 32 / KJ;  // lanes that hold the same total
-  if (wpt == 1) {
-    if (at.t < T && lane % W == 0 && lane / W < k)
+  const float sum = scale * reduce_lanes<KJ, L>(dot);
+  constexpr int W = L / KJ;  // lanes that hold the same total
+  if (warp_bits == 0) {
+    if (t < T && lane % W == 0 && lane / W < k)
       dgate[t * k + lane / W] = pos[t * k + lane / W] >= 0 ? sum : 0.f;
     return;
   }
   if (lane % W == 0) part[warp][lane / W] = sum;
   __syncthreads();
-  if (at.t < T && at.part == 0 && lane < k) {
+  if (t < T && at.part == 0 && lane < k) {
     float total = 0.f;
-    for (int i = 0; i < wpt; ++i) total += part[warp + i][lane];
+    for (int i = 0; i < 1 << warp_bits; ++i) total += part[warp + i][lane];
     dgate[t * k + lane] = pos[t * k + lane] >= 0 ? total : 0.f;
   }
 }
 
-// Warps a token, for kernels whose warps sweep 32 CH chunks of a row at a
-// time: as many as leave each four sweeps; and where the tokens are too few
-// to fill the GPU (eight warps on each of 148 SMs), as many as leave each one.
-int warps_per_token(int T, int d, int ch) {
+// log2 of the warps a row, for kernels whose warps sweep 32 `ch` chunks of a
+// row at a time: as many as leave each four sweeps; and where the tokens are
+// too few to fill the GPU (eight warps on each of 148 SMs), as many as leave
+// each one.
+int pick_warp_bits(int T, int d, int ch) {
   const int sweeps = (d / 8 + 32 * ch - 1) / (32 * ch);
-  int wpt = 1;
-  while (wpt < kCdWarps &&
-         (sweeps >= 8 * wpt ||
-          (static_cast<int64_t>(T) * wpt < 148 * kCdWarps && sweeps >= 2 * wpt)))
-    wpt *= 2;
-  return wpt;
+  int bits = 0;
+  while ((1 << bits) < kCdWarps &&
+         (sweeps >= 8 << bits ||
+          (static_cast<int64_t>(T) << bits < 148 * kCdWarps && sweeps >= 2 << bits)))
+    ++bits;
+  return bits;
+}
+
+// Rows of at most 16 chunks take eight lanes of a warp, so that its other
+// lanes work on other rows (100000 x 64, top-2: forward 39.7 -> 10.0 us,
+// backward 48.0 -> 12.3; with a row width known only at run time the wide rows
+// lose: 98 -> 115 us on 16384 x 2048 top-8).
+bool narrow(int d) { return d <= 128; }
+
+template <bool BACKWARD, bool BF16, int KJ, int CH, int L>
+cudaError_t launch(const CombineDropoutArgs& a, cudaStream_t s) {
+  const int warp_bits = L == 32 ? pick_warp_bits(a.T, a.d, CH) : 0;
+  const int tokens = tokens_per_cta(L, warp_bits);
+  const dim3 grid((static_cast<unsigned>(a.T) + tokens - 1) / tokens), block(kCdWarps * 32);
+  if constexpr (BACKWARD)
+    return launch_kernel(combine_dropout_backward_kernel<BF16, KJ, CH, L>, grid, block, 0, s, 1,
+                         true, a.dy, a.o, a.pos, a.gate, a.rng, a.threshold, a.scale, a.T, a.d,
+                         a.k, warp_bits, a.d_o, a.dgate);
+  else
+    return launch_kernel(combine_dropout_kernel<BF16, KJ, CH, L>, grid, block, 0, s, 1, true, a.o,
+                         a.pos, a.gate, a.residual, a.rng, a.threshold, a.scale, a.T, a.d, a.k,
+                         warp_bits, a.y);
+}
+
+// Two chunks a lane and sweep where the registers hold them: of up to two
+// slots in bf16, in the backward pass of up to four (8192 x 4096 top-4: 111 us
+// with one chunk, 96 with two; forward 60.4 and 62.2).  A kernel for four
+// slots of its own, since the absent ones of eight hold registers and issue
+// slots (8192 x 4096 top-4: 66 and 115 us; 16384 x 512 top-4 forward 21.2 us
+// against 15.6).
+template <bool BACKWARD, bool BF16>
+cudaError_t pick(const CombineDropoutArgs& a, cudaStream_t s) {
+  constexpr int C2 = BF16 ? 2 : 1, C4 = BF16 && BACKWARD ? 2 : 1;
+  if (narrow(a.d))
+    return a.k <= 2   ? launch<BACKWARD, BF16, 2, 1, 8>(a, s)
+           : a.k <= 4 ? launch<BACKWARD, BF16, 4, 1, 8>(a, s)
+                      : launch<BACKWARD, BF16, kMaxK, 1, 8>(a, s);
+  return a.k <= 2   ? launch<BACKWARD, BF16, 2, C2, 32>(a, s)
+         : a.k <= 4 ? launch<BACKWARD, BF16, 4, C4, 32>(a, s)
+                    : launch<BACKWARD, BF16, kMaxK, 1, 32>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_combine_dropout(const CombineDropoutArgs& a, moe_dtype dtype, cudaStream_t s) {
-  auto go = [&](auto kern, int ch) {
-    const int wpt = warps_per_token(a.T, a.d, ch), tokens = kCdWarps / wpt;
-    const dim3 grid((static_cast<unsigned>(a.T) + tokens - 1) / tokens);
-    return launch_kernel(kern, grid, dim3(kCdWarps * 32), 0, s, 1, true, a.o, a.pos, a.gate,
-                         a.residual, a.rng, a.threshold, a.scale, a.T, a.d, a.k, wpt, a.y);
-  };
-  if (dtype == MOE_BF16)
-    return a.k <= 2 ? go(combine_dropout_kernel<true, 2, 2>, 2)
-                    : go(combine_dropout_kernel<true, kMaxK, 1>, 1);
-  return a.k <= 2 ? go(combine_dropout_kernel<false, 2, 1>, 1)
-                  : go(combine_dropout_kernel<false, kMaxK, 1>, 1);
+  return dtype == MOE_BF16 ? pick<false, true>(a, s) : pick<false, false>(a, s);
 }
 
 cudaError_t launch_combine_dropout_backward(const CombineDropoutArgs& a, moe_dtype dtype,
                                             cudaStream_t s) {
-  auto go = [&](auto kern, int ch) {
-    const int wpt = warps_per_token(a.T, a.d, ch), tokens = kCdWarps / wpt;
-    const dim3 grid((static_cast<unsigned>(a.T) + tokens - 1) / tokens);
-    return launch_kernel(kern, grid, dim3(kCdWarps * 32), 0, s, 1, true, a.dy, a.o, a.pos, a.gate,
-                         a.rng, a.threshold, a.scale, a.T, a.d, a.k, wpt, a.d_o, a.dgate);
-  };
-  if (dtype == MOE_BF16)
-    return a.k <= 2 ? go(combine_dropout_backward_kernel<true, 2, 2>, 2)
-                    : go(combine_dropout_backward_kernel<true, kMaxK, 1>, 1);
-  return a.k <= 2 ? go(combine_dropout_backward_kernel<false, 2, 1>, 1)
-                  : go(combine_dropout_backward_kernel<false, kMaxK, 1>, 1);
+  return dtype == MOE_BF16 ? pick<true, true>(a, s) : pick<true, false>(a, s);
 }
 
 }  // namespace moe

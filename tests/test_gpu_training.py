@@ -368,6 +368,13 @@ COMBINE = [
     (255, 1032, 16, 3, "fp32", 0.0, True, 0), (300, 2056, 32, 4, "bf16", 0.99999, True, None),
     (1000, 136, 64, 8, "bf16", 0.1, False, 60), (1300, 1024, 8, 2, "bf16", 1e-6, True, None),
     (2049, 64, 12, 5, "fp32", 0.5, True, None),
+    # rows of eight lanes (up to 128 elements), and one element group more
+    (1001, 64, 8, 2, "bf16", 0.1, True, None), (45, 72, 7, 3, "fp32", 0.4, True, 20),
+    (77, 128, 16, 4, "bf16", 0.1, False, None), (515, 128, 64, 7, "bf16", 0.0, True, 50),
+    (31, 8, 3, 1, "fp32", 0.5, True, None), (90, 136, 9, 4, "bf16", 0.2, True, 30),
+    # three and four slots, rows of several warps
+    (5, 4096, 8, 3, "bf16", 0.1, True, None), (2000, 4104, 8, 4, "bf16", 0.1, True, 700),
+    (900, 1544, 6, 4, "fp32", 0.1, False, None),
 ]
 CIDS = ["x".join(map(str, c[:4])) + "-" + c[4] for c in COMBINE]
 
