@@ -325,9 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t t1 = min(static_cast<uint32_t>(a.T),
                           static_cast<uint32_t>(static_cast<int64_t>(blockIdx.y + 1) * tiles /
                                                 ranges) * kTile);
-  pdl_wait();
-  pdl_trigger();
-  auto load = [&](uint32_t tb, int st) {
+  auto load_x = [&](uint32_t tb, int st) {
     const int rows = min(static_cast<uint32_t>(kTile), t1 - tb);
     if (a.dWg)
 #pragma unroll
@@ -337,6 +335,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         cp_async16(smem_u32(&sm.x[st][r][4 * cg]),
                    use ? x + static_cast<int64_t>(tb + r) * a.d + col : x, use ? 16 : 0);
       }
+  };
+  auto load_dz = [&](uint32_t tb, int st) {
+    const int rows = min(static_cast<uint32_t>(kTile), t1 - tb);
     const float* from = dz + static_cast<int64_t>(tb) * EP;
 #pragma unroll
     for (int i = tid; i < kTile * EP / 4; i += kThreads) {
@@ -345,7 +346,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     cp_async_commit();
   };
-  if (t0 < t1) load(t0, 0);
+  // The dz kernel has waited for everything before it, so the call's inputs
+  // may be read before its end.
+  if (t0 < t1) load_x(t0, 0);
   if (dx) {
     for (int i = tid; i < EP * kCols; i += kThreads) (&sm.w[0][0])[i] = 0.f;
     __syncthreads();
@@ -358,13 +361,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (e >= a.E) e -= a.E, ++c;
     }
   }
+  pdl_wait();
+  pdl_trigger();
+  if (t0 < t1) load_dz(t0, 0);
   const int eg = tid / 16 % EG, tg = tid / (16 * EG);
   float acc[4][4] = {};
   int st = 0;
   for (uint32_t tb = t0; tb < t1; tb += kTile, st ^= 1) {
     const int rows = min(static_cast<uint32_t>(kTile), t1 - tb);
     if (tb + kTile < t1)
-      load(tb + kTile, st ^ 1);
+      load_x(tb + kTile, st ^ 1), load_dz(tb + kTile, st ^ 1);
     else
       cp_async_commit();  // one group a tile, so that the wait counts tiles
     // This thread's four tokens and columns of dx.
