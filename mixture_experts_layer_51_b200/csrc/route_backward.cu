@@ -299,7 +299,8 @@ template <int EP>
 struct SimtSmem {
   float x[2][kTile][kCols];
   float dz[2][kTile][EP];
-  float w[EP][kCols];        // W_g of the columns, expert-major
+  float w[EP][kCols + 4];    // W_g of the columns, expert-major; padded: a warp's
+                             // stores of a column's experts would share a bank
   float4 scratch[kThreads];
   uint32_t last;
 };
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // may be read before its end.
   if (t0 < t1) load_x(t0, 0);
   if (dx) {
-    for (int i = tid; i < EP * kCols; i += kThreads) (&sm.w[0][0])[i] = 0.f;
+    for (int i = tid; i < EP * (kCols + 4); i += kThreads) (&sm.w[0][0])[i] = 0.f;
     __syncthreads();
     int c = tid / a.E, e = tid % a.E;
     const int dc = kThreads / a.E, de = kThreads % a.E;
@@ -431,20 +432,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       sum_bias(sums, e, tid);
   if (!a.dWg) return;
   // The token groups' parts, in order, then the range's part to memory.
-  float* part = &sm.x[0][0][0];  // [TG][64 columns][EP]: 16 KB
+  // Parts [TG][64 columns][EP], 16 KB, in pieces of 16 bytes whose place is
+  // xored with the column group, so that a warp's stores miss one another's
+  // banks.
+  float* part = &sm.x[0][0][0];
+  auto place = [](int column, int e) {  // of all token groups' columns
+    return ((column * EG + e / 4) ^ (column / 4 & 7)) * 4 + e % 4;
+  };
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) part[(tg * kCols + 4 * cg + i) * EP + 4 * eg + e] = acc[i][e];
+    *reinterpret_cast<float4*>(part + place(tg * kCols + 4 * cg + i, 4 * eg)) =
+        make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
   __syncthreads();
   {
     float* out = sums.dw + (static_cast<int64_t>(blockIdx.y) * a.d + c0) * a.E;
     int c = tid / a.E, e = tid % a.E;
     const int dc = kThreads / a.E, de = kThreads % a.E;
     for (int i = tid; i < cols * a.E; i += kThreads) {
-      float sum = part[c * EP + e];
+      float sum = part[place(c, e)];
 #pragma unroll
-      for (int g = 1; g < TG; ++g) sum += part[(g * kCols + c) * EP + e];
+      for (int g = 1; g < TG; ++g) sum += part[place(g * kCols + c, e)];
       out[i] = sum;
       c += dc;
       e += de;
