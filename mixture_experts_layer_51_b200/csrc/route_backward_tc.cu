@@ -21,10 +21,10 @@
 // raises the workspace's error word and the CTA leaves after its copies and
 // MMAs have landed.
 //
-// Measured on one B200, both launches of the backward pass (floors at
-// 6.56 TB/s in brackets): 8192 x 4096, 8 experts, with dx_acc 39.6 us (30.8),
-// without 30.0 (20.6); 16384 x 2048 without dx_acc: 32 experts 39.0 us, 64
-// experts 41.2 (21.3), 41.9 with a mask that leaves out one token in six.  A
+// Measured on one B200, all launches of the backward pass (floors at
+// 6.56 TB/s in brackets): 8192 x 4096, 8 experts, with dx_acc 39.8 us (30.8),
+// without 29.6 (20.6); 16384 x 2048 without dx_acc: 32 experts 36.6 us, 64
+// experts 39.6 (21.3), 40.0 with a mask that leaves out one token in six.  A
 // tile takes 1.45 us there, what its 64 KB take at the HBM rate of 144 CTAs;
 // the rest is the dz kernel (7 us, which the first tiles' x is loaded behind)
 // and about 7 us of start, last tile and sums.  On fp32 FMA the same passes
