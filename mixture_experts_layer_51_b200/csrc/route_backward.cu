@@ -293,9 +293,11 @@ __global__ void __launch_bounds__(kDzThreads, 4)
 // range of tokens, in tiles of 64 tokens that cp.async brings two stages deep.
 // Register tiles of 4 x 4 in both products (columns x experts over the tokens;
 // tokens x columns over the experts) take two 16-byte shared-memory reads for
-// 16 FMA, which bounds the tiles of many experts (4096 x 1024: 8 experts
-// 13.8 us for the pass, 7.7 at 6.56 TB/s; 64 experts 41 us, the reads' pipe at
-// three quarters of its rate on the busiest SMs).  With fewer than 64 experts the threads that dW_g does not need
+// 16 FMA (4096 x 1024: 8 experts 13.8 us for the pass, 7.7 at 6.56 TB/s; 64
+// experts 41 us, the reads' pipe at three quarters of its rate on the busiest
+// SMs; tiles of 8 x 8 and 8 x 4 on 128 columns leave one CTA an SM and took 40.5
+// there, but 44.5 us against 43.3 for 2048 x 4096 with 32 experts and 21 against
+// 16 for 700 x 256 with 64).  With fewer than 64 experts the threads that dW_g does not need
 // share out the tile's tokens, and are added up when the range is done.
 template <int EP>
 struct SimtSmem {
