@@ -545,6 +545,7 @@ moe_status moe_balance_loss(const float* scores, const int32_t* idx, const uint8
  *   gates, MOE_GATE_SOFTMAX_TOPK: at idx_j   g_j dg_j, and everywhere
  *                                 - p_e sum_i g_i dg_i
  *   loss:  dloss coef (E / N) p_e (f_e - sum_i f_i p_i)
+ *   T <= 2^31 - 128.
  *   x [T, d], Wg [d, E] (dtype); scores [E, T] (may be NULL where neither
  *   counts nor MOE_GATE_SOFTMAX_TOPK reads it); idx, gate, dgate [T, k] or
  *   dgate NULL: nothing through the gates (idx and gate are then not read;

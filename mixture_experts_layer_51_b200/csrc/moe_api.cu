@@ -1053,6 +1053,12 @@ bool valid_combine_sizes(int32_t T, int32_t d, int32_t k, moe_dtype dt) {
   return T >= 0 && d > 0 && d % 8 == 0 && k >= 1 && k <= kMaxK && valid_dtype(dt);
 }
 
+// The router's backward pass takes tokens in tiles of up to 128, whose ends
+// have to be int32 too.
+bool valid_route_backward_sizes(int32_t T, int32_t d, int32_t E, int32_t k) {
+  return valid_route_sizes(T, d, E, k) && T <= INT32_MAX - 127;
+}
+
 }  // namespace
 
 MOE_API size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E) {
@@ -1080,7 +1086,7 @@ MOE_API moe_status moe_balance_loss(const float* scores, const int32_t* idx, con
 }
 
 MOE_API size_t moe_route_backward_workspace_bytes(int32_t T, int32_t d, int32_t E, moe_dtype dt) {
-  return valid_route_sizes(T, d, E, 1) && valid_dtype(dt)
+  return valid_route_backward_sizes(T, d, E, 1) && valid_dtype(dt)
              ? route_backward_scratch_bytes(T, d, E, dt)
              : 0;
 }
@@ -1095,7 +1101,7 @@ MOE_API moe_status moe_route_backward(const void* x, const void* Wg, const float
                                       void* stream) {
   int gating;
   float gate_scale;
-  if (!valid_route_sizes(T, d, E, k) || !valid_dtype(dt) ||
+  if (!valid_route_backward_sizes(T, d, E, k) || !valid_dtype(dt) ||
       !read_options(opt, &gating, &gate_scale) || !isfinite(coef))
     return MOE_ERR_ARG;
   if (!aligned16(dx) || !aligned16(dWg) || !aligned4(dbias)) return MOE_ERR_ARG;

@@ -52,7 +52,7 @@ def _route_back(lib, **kw):
     dict(tokens=None), dict(counts=ODD), dict(tokens=ODD), dict(dloss=ODD), dict(idx=None),
     dict(gate=None), dict(idx=ODD), dict(gate=ODD), dict(dgate=ODD), dict(scores=None),
     dict(scores=ODD), dict(Wg=None), dict(Wg=HALF), dict(dx_acc=HALF), dict(x=None), dict(x=HALF),
-    dict(ws=None), dict(ws=HALF), dict(ws_bytes=16)])
+    dict(ws=None), dict(ws=HALF), dict(ws_bytes=16), dict(T=2**31 - 127)])
 def test_route_backward_refuses(lib, bad):
     assert _route_back(lib, **bad) == M.MOE_ERR_ARG
 
@@ -121,6 +121,9 @@ def test_workspace_sizes(lib):
         100000, 8)
     assert M.moe_route_backward_workspace_bytes(10, 12, 8, torch.bfloat16) == 0
     assert M.moe_route_backward_workspace_bytes(10, 64, 65, torch.bfloat16) == 0
+    # the end of the last tile of tokens is an int32 too
+    assert M.moe_route_backward_workspace_bytes(2**31 - 127, 64, 8, torch.float32) == 0
+    assert M.moe_route_backward_workspace_bytes(2**31 - 128, 64, 8, torch.float32) >= 2**31 * 4
     for dt in (torch.bfloat16, torch.float32):
         # room for dz at least, and bounded by a few copies of dz and dWg
         need = M.moe_route_backward_workspace_bytes(10000, 2048, 64, dt)
