@@ -10,14 +10,15 @@
 //   dx = dx_acc + dz W_g^T,   dW_g = x^T dz,   dbias = sum_t dz
 //
 // Small batches go to route_backward_small.cu in one launch; the others take
-// two launches or three.  (1) dz for every token, and its column sums per block of
-// tokens.  (2) Both products in one pass over x: a CTA owns a block of
-// columns and a range of tokens, so each x element is read once, each dx
+// two launches or three.  (1) dz for every token, and its column sums per
+// block of tokens.  (2) Both products in one pass over x: a CTA owns a block
+// of columns and a range of tokens, so each x element is read once, each dx
 // element written once, and dW_g of the block stays on the chip until the
 // range is done (bf16: tensor cores, route_backward_tc.cu; fp32: FMA, here).
-// The last range of a column block to finish adds all of the block's ranges
-// in order, or a third launch does, and one warp an expert adds the dz blocks'
-// column sums: no sum depends on scheduling (no floating-point atomics).
+// (3) With many ranges, their sum; with few, the last range of a column block
+// to finish adds all of the block's.  Either goes in order, and one warp an
+// expert adds the dz blocks' column sums: no sum depends on scheduling (no
+// floating-point atomics).
 //
 // dz is a launch of its own because every column block needs it: 5.6 MB of
 // scores and gates in, 128 to 384 bytes a token out (bf16 terms), 7 us for

@@ -11,13 +11,13 @@
 // up in order), 2 tokens x 4 columns over the experts for dx.
 //
 // Where it is taken: up to 256 tokens and 4096 dz values (experts rounded up
-// to 8, 16, 32 or 64), and no more CTAs than SMs.  Measured in a graph on one B200 against the two launches of
-// route_backward.cu (bf16): 256 x 64, 4 experts 5.7 us (7.1); 256 x 4096, 8
-// experts 6.4 (8.9), 16 experts 8.2 (9.1); 128 x 4096, 32 experts 7.9 (10.0);
-// 64 x 4096, 64 experts 9.5 (10.3); past the rule 256 x 1024, 32 experts 11.0
-// (10.4), 128 x 1024, 64 experts 11.8 (10.5), where the products' shared
-// memory reads bound it, and 256 x 8192, 8 experts 11.3 (9.0), with two CTAs
-// an SM.  The host saves 2.5 us a call.
+// to 8, 16, 32 or 64), and no more CTAs than SMs.  Measured in a graph on one
+// B200 against the two launches of route_backward.cu (bf16): 256 x 64, 4
+// experts 5.7 us (7.1); 256 x 4096, 8 experts 6.4 (8.9), 16 experts 8.2 (9.1);
+// 128 x 4096, 32 experts 7.9 (10.0); 64 x 4096, 64 experts 9.5 (10.3); past the
+// rule 256 x 1024, 32 experts 11.0 (10.4), 128 x 1024, 64 experts 11.8 (10.5),
+// where the products' shared memory reads bound it, and 256 x 8192, 8 experts
+// 11.3 (9.0), with two CTAs an SM.  The host saves 2.5 us a call.
 
 #include "route_backward.cuh"
 
