@@ -56,14 +56,18 @@ int pick_ranges(int cols, int tiles, int per_sm) {
 
 // The ranges of dW_g are added by the last CTA of a column block, or by a
 // launch over all SMs.  The launch is quicker on the GPU from about five
-// ranges on (16384 x 2048, 64 experts, 9 ranges: 39.8 us for the pass against
-// 42.1; 4096 x 1024 fp32, 16 ranges: 15.0 against 18.1; 16384 x 64, 64
+// ranges on (16384 x 2048, 64 experts, 9 ranges: 40.0 us for the pass against
+// 42.1; 16384 x 1024, 8 experts, 18 ranges: 18.9 against 22.6; 16384 x 64, 64
 // experts, 128 ranges: 13.7 against 51; at four ranges both take 39.8 us), but
-// costs the host 2.3 us.  So passes that the host bounds anyway (x of less
-// than 8 MB) do without, as long as one CTA has no more than 20 to add.
+// costs the host 2.3 us.  A call from Python takes the host about 16 us
+// without it, so passes that the GPU is through with in that time (x of less
+// than 8 M elements) do without, as long as one CTA has no more than 20 to add
+// (4096 x 1024 fp32, 16 ranges: a call among others 18.4 us with the launch
+// and 16.6 without, 13.8 and 16.7 on the GPU; 8192 x 1024, 16 experts, 18
+// ranges: 18.4 and 18.9, 14.1 and 18.9 on the GPU).
 constexpr int kFewRanges = 4;
 constexpr int kPassingRanges = 20;
-constexpr int64_t kSummingLaunchBytes = 8 << 20;
+constexpr int64_t kSummingLaunchElements = 8 << 20;
 
 RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   RouteBackwardPlan p{};
@@ -75,8 +79,7 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   p.tiles = (T + tile - 1) / tile;
   p.ranges = T > 0 ? pick_ranges(p.cols, p.tiles, tc ? 1 : 2) : 0;
   p.many = p.ranges > kPassingRanges ||
-           (p.ranges > kFewRanges &&
-            static_cast<int64_t>(T) * d * (tc ? 2 : 4) >= kSummingLaunchBytes);
+           (p.ranges > kFewRanges && static_cast<int64_t>(T) * d >= kSummingLaunchElements);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(kDzThreads, 4)
 // range of tokens, in tiles of 64 tokens that cp.async brings two stages deep.
 // Register tiles of 4 x 4 in both products (columns x experts over the tokens;
 // tokens x columns over the experts) take two 16-byte shared-memory reads for
-// 16 FMA (4096 x 1024: 8 experts 13.8 us for the pass, 7.7 at 6.56 TB/s; 64
+// 16 FMA (4096 x 1024: 8 experts 16.7 us for the pass, 7.7 at 6.56 TB/s; 64
 // experts 41 us, the reads' pipe at three quarters of its rate on the busiest
 // SMs; tiles of 8 x 8 and 8 x 4 on 128 columns leave one CTA an SM and took 40.5
 // there, but 44.5 us against 43.3 for 2048 x 4096 with 32 experts and 21 against

@@ -144,7 +144,8 @@ ROUTE = [
     (20000, 64, 44, 2, "bf16", "topk_softmax", 1.0, True, True, "some", False),
     (20000, 64, 8, 2, "fp32", "softmax_topk", 1.0, True, True, "some", True),
     (9000, 520, 30, 2, "bf16", "topk_softmax", 1.0, False, True, None, False),
-    (5000, 1160, 6, 2, "bf16", "topk_softmax", 1.0, False, True, None, True),
+    (8200, 1160, 6, 2, "bf16", "topk_softmax", 1.0, False, True, None, True),
+    (8200, 1032, 50, 3, "fp32", "softmax_topk", 1.0, True, True, "some", True),
     # around the sizes up to which one launch does it all
     (256, 264, 8, 2, "bf16", "softmax_topk", 1.0, True, True, "some", True),
     (256, 264, 16, 4, "fp32", "topk_softmax", 2.0, True, True, "some", True),
