@@ -663,7 +663,7 @@ class MoELayer:
         backward_router read (xp, h, o, offsets and kept_counts among them,
         for a backward pass of the experts).  x and rng are held, not copied:
         neither may change before the backward pass."""
-        _tensor(x, "x", self.dtype, (x.shape[0], self.d), self.device)
+        _tensor(x, "x", self.dtype, (x.shape[0], self.d), self.device.index)
         idx, gate, _ = moe_route(x, self.Wg, self.bias, self.k, gating=self.gating,
                                  gate_scale=self.gate_scale)
         scores = moe_expert_choice_route(x, self.Wg, self.bias)
@@ -696,7 +696,7 @@ class MoELayer:
         own backward pass; dx then holds both."""
         dx_acc = None
         if dxp is not None and "dx" in outputs:
-            _tensor(dxp, "dxp", self.dtype, step["xp"].shape, self.device)
+            _tensor(dxp, "dxp", self.dtype, step["xp"].shape, self.device.index)
             dx_acc = moe_unpermute_combine(dxp, step["pos"], torch.ones_like(step["gate"]),
                                            step["x"].dtype)
         return moe_route_backward(step["x"], self.Wg, step["idx"], step["gate"], step["dgate"],
@@ -711,27 +711,27 @@ class MoELayer:
 
 
 # ---------------------------------------------------------------- training
-def _tensor(t, name, dtype, shape, dev):
+def _tensor(t, name, dtype, shape, index):
     """The address of an argument that the kernels will read or write: its
-    type, shape, device and dense layout are checked here, because a raw
-    pointer carries none of them.  None passes as NULL."""
+    type, shape, CUDA device (by index) and dense layout are checked here,
+    because a raw pointer carries none of them.  None passes as NULL."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     raise ValueError(f"{name} is not contiguous")
 
 
-def _mask(mask, T, dev):
+def _mask(mask, T, index):
     """A bool or uint8 mask's address (a torch bool is one byte, 0 or 1)."""
     kind = torch.uint8 if mask is not None and mask.dtype is torch.uint8 else torch.bool
-    return _tensor(mask, "mask", kind, (T,), dev)
+    return _tensor(mask, "mask", kind, (T,), index)
 
 
 def _cuda_device(t, name):
@@ -753,13 +753,14 @@ def _route_options(gating, gate_scale):
     return ctypes.byref(_options(gating, gate_scale))
 
 
-def _launch(fn, where, dev, stream, *args):
-    """fn(*args, stream) with ``dev`` current (its own stream if none is given)."""
-    s = stream.cuda_stream if stream is not None else _raw_stream(dev.index)
-    if _current_device() == dev.index:
+def _launch(fn, where, index, stream, *args):
+    """fn(*args, stream) with device ``index`` current (its own current stream
+    if none is given)."""
+    s = stream.cuda_stream if stream is not None else _raw_stream(index)
+    if _current_device() == index:
         status = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             status = fn(*args, s)
     if status != MOE_OK:
         raise MoeError(status, where)
@@ -797,6 +798,7 @@ def moe_balance_loss(scores, idx, coef, mask=None, loss=None, prob_sum=None, cou
     E, T = scores.shape
     k = idx.shape[1]
     dev = _cuda_device(scores, "scores")
+    at = dev.index
     i32, f32 = torch.int32, torch.float32
     loss = loss if loss is not None else _empty(1, f32, dev, stream)
     prob_sum = prob_sum if prob_sum is not None else _empty(E, f32, dev, stream)
@@ -804,11 +806,11 @@ def moe_balance_loss(scores, idx, coef, mask=None, loss=None, prob_sum=None, cou
     tokens = tokens if tokens is not None else _empty(1, i32, dev, stream)
     ws = _workspace(ws, 0 if ws is not None else moe_balance_loss_workspace_bytes(T, E), dev,
                     stream)
-    _launch(lib().moe_balance_loss, "moe_balance_loss", dev, stream,
-            _tensor(scores, "scores", f32, (E, T), dev), _tensor(idx, "idx", i32, (T, k), dev),
-            _mask(mask, T, dev), T, E, k, coef,
-            _tensor(loss, "loss", f32, (1,), dev), _tensor(prob_sum, "prob_sum", f32, (E,), dev),
-            _tensor(counts, "counts", i32, (E,), dev), _tensor(tokens, "tokens", i32, (1,), dev),
+    _launch(lib().moe_balance_loss, "moe_balance_loss", at, stream,
+            _tensor(scores, "scores", f32, (E, T), at), _tensor(idx, "idx", i32, (T, k), at),
+            _mask(mask, T, at), T, E, k, coef,
+            _tensor(loss, "loss", f32, (1,), at), _tensor(prob_sum, "prob_sum", f32, (E,), at),
+            _tensor(counts, "counts", i32, (E,), at), _tensor(tokens, "tokens", i32, (1,), at),
             ws.data_ptr(), ws.numel() * ws.element_size())
     return dict(loss=loss, prob_sum=prob_sum, counts=counts, tokens=tokens)
 
@@ -833,6 +835,7 @@ def moe_route_backward(x, Wg, idx, gate=None, dgate=None, scores=None, counts=No
     E = Wg.shape[1]
     k = idx.shape[1]
     dev = _cuda_device(x, "x")
+    at = dev.index
     i32, f32, dt = torch.int32, torch.float32, x.dtype
     code = _dtype_code(x)
     out = {}
@@ -852,17 +855,17 @@ def moe_route_backward(x, Wg, idx, gate=None, dgate=None, scores=None, counts=No
         raise ValueError(f"outputs {outputs}: dx, dWg and dbias, each at most once")
     ws = _workspace(ws, 0 if ws is not None else
                     moe_route_backward_workspace_bytes(T, d, E, dt), dev, stream)
-    _launch(lib().moe_route_backward, "moe_route_backward", dev, stream,
-            _tensor(x, "x", dt, (T, d), dev), _tensor(Wg, "Wg", dt, (d, E), dev),
-            _tensor(scores, "scores", f32, (E, T), dev), _tensor(idx, "idx", i32, (T, k), dev),
-            _tensor(gate, "gate", f32, (T, k), dev), _tensor(dgate, "dgate", f32, (T, k), dev),
-            _tensor(counts, "counts", i32, (E,), dev), _tensor(tokens, "tokens", i32, (1,), dev),
-            _tensor(dloss, "dloss", f32, (1,), dev), coef,
-            _mask(mask, T, dev),
-            _tensor(dx_acc, "dx_acc", dt, (T, d), dev), T, d, E, k, code,
+    _launch(lib().moe_route_backward, "moe_route_backward", at, stream,
+            _tensor(x, "x", dt, (T, d), at), _tensor(Wg, "Wg", dt, (d, E), at),
+            _tensor(scores, "scores", f32, (E, T), at), _tensor(idx, "idx", i32, (T, k), at),
+            _tensor(gate, "gate", f32, (T, k), at), _tensor(dgate, "dgate", f32, (T, k), at),
+            _tensor(counts, "counts", i32, (E,), at), _tensor(tokens, "tokens", i32, (1,), at),
+            _tensor(dloss, "dloss", f32, (1,), at), coef,
+            _mask(mask, T, at),
+            _tensor(dx_acc, "dx_acc", dt, (T, d), at), T, d, E, k, code,
             _route_options(gating, gate_scale),
-            _tensor(dx, "dx", dt, (T, d), dev), _tensor(dWg, "dWg", f32, (d, E), dev),
-            _tensor(dbias, "dbias", f32, (E,), dev), ws.data_ptr(),
+            _tensor(dx, "dx", dt, (T, d), at), _tensor(dWg, "dWg", f32, (d, E), at),
+            _tensor(dbias, "dbias", f32, (E,), at), ws.data_ptr(),
             ws.numel() * ws.element_size())
     return out
 
@@ -875,15 +878,16 @@ def moe_combine_dropout(o, pos, gate, p=0.0, rng=None, residual=None, y=None, st
     T, k = pos.shape
     rows, d = o.shape
     dev = _cuda_device(o, "o")
+    at = dev.index
     dt = o.dtype
     code = _dtype_code(o)
     y = y if y is not None else _empty((T, d), dt, dev, stream)
-    _launch(lib().moe_combine_dropout, "moe_combine_dropout", dev, stream,
-            _tensor(o, "o", dt, (rows, d), dev), _tensor(pos, "pos", torch.int32, (T, k), dev),
-            _tensor(gate, "gate", torch.float32, (T, k), dev),
-            _tensor(residual, "residual", dt, (T, d), dev), p,
-            _tensor(rng, "rng", torch.int64, (2,), dev), T, d, k, code,
-            _tensor(y, "y", dt, (T, d), dev))
+    _launch(lib().moe_combine_dropout, "moe_combine_dropout", at, stream,
+            _tensor(o, "o", dt, (rows, d), at), _tensor(pos, "pos", torch.int32, (T, k), at),
+            _tensor(gate, "gate", torch.float32, (T, k), at),
+            _tensor(residual, "residual", dt, (T, d), at), p,
+            _tensor(rng, "rng", torch.int64, (2,), at), T, d, k, code,
+            _tensor(y, "y", dt, (T, d), at))
     return y
 
 
@@ -895,17 +899,18 @@ def moe_combine_dropout_backward(dy, o, pos, gate, p=0.0, rng=None, d_o=None, dg
     T, k = pos.shape
     rows, d = o.shape
     dev = _cuda_device(o, "o")
+    at = dev.index
     dt = o.dtype
     code = _dtype_code(o)
     d_o = d_o if d_o is not None else _empty((rows, d), dt, dev, stream)
     dgate = dgate if dgate is not None else _empty((T, k), torch.float32, dev, stream)
-    _launch(lib().moe_combine_dropout_backward, "moe_combine_dropout_backward", dev, stream,
-            _tensor(dy, "dy", dt, (T, d), dev), _tensor(o, "o", dt, (rows, d), dev),
-            _tensor(pos, "pos", torch.int32, (T, k), dev),
-            _tensor(gate, "gate", torch.float32, (T, k), dev), p,
-            _tensor(rng, "rng", torch.int64, (2,), dev), T, d, k, code,
-            _tensor(d_o, "d_o", dt, (rows, d), dev),
-            _tensor(dgate, "dgate", torch.float32, (T, k), dev))
+    _launch(lib().moe_combine_dropout_backward, "moe_combine_dropout_backward", at, stream,
+            _tensor(dy, "dy", dt, (T, d), at), _tensor(o, "o", dt, (rows, d), at),
+            _tensor(pos, "pos", torch.int32, (T, k), at),
+            _tensor(gate, "gate", torch.float32, (T, k), at), p,
+            _tensor(rng, "rng", torch.int64, (2,), at), T, d, k, code,
+            _tensor(d_o, "d_o", dt, (rows, d), at),
+            _tensor(dgate, "dgate", torch.float32, (T, k), at))
     return d_o, dgate
 
 
