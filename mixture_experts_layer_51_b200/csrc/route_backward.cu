@@ -61,13 +61,16 @@ int pick_ranges(int cols, int tiles, int per_sm) {
 // experts, 128 ranges: 13.7 against 51; at four ranges both take 39.8 us), but
 // costs the host 2.3 us.  A call from Python takes the host about 16 us
 // without it, so passes that the GPU is through with in that time (x of less
-// than 8 M elements) do without, as long as one CTA has no more than 20 to add
-// (4096 x 1024 fp32, 16 ranges: a call among others 18.4 us with the launch
-// and 16.6 without, 13.8 and 16.7 on the GPU; 8192 x 1024, 16 experts, 18
-// ranges: 18.4 and 18.9, 14.1 and 18.9 on the GPU).
+// than 16 MB) do without, as long as one CTA has no more than 20 to add
+// (2048 x 2048, 8 experts, 9 ranges: 11.0 us on the GPU with the launch and
+// 12.0 without).  At 16 MB a call takes as long either way, or less with the
+// launch, and the GPU is done earlier (4096 x 1024 fp32, 16 ranges, inputs not
+// in L2: 17.8 to 18.6 us a call with it and 18.3 without; from L2 13.8 and 16.7 on
+// the GPU; 8192 x 1024, 16 experts, 18 ranges: 18.2 and 18.9 a call, 14.1 and
+// 18.9 on the GPU).
 constexpr int kFewRanges = 4;
 constexpr int kPassingRanges = 20;
-constexpr int64_t kSummingLaunchElements = 8 << 20;
+constexpr int64_t kSummingLaunchBytes = 16 << 20;
 
 RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   RouteBackwardPlan p{};
@@ -79,7 +82,8 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   p.tiles = (T + tile - 1) / tile;
   p.ranges = T > 0 ? pick_ranges(p.cols, p.tiles, tc ? 1 : 2) : 0;
   p.many = p.ranges > kPassingRanges ||
-           (p.ranges > kFewRanges && static_cast<int64_t>(T) * d >= kSummingLaunchElements);
+           (p.ranges > kFewRanges &&
+            static_cast<int64_t>(T) * d * (tc ? 2 : 4) >= kSummingLaunchBytes);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kDzThreads, 4)
 // range of tokens, in tiles of 64 tokens that cp.async brings two stages deep.
 // Register tiles of 4 x 4 in both products (columns x experts over the tokens;
 // tokens x columns over the experts) take two 16-byte shared-memory reads for
-// 16 FMA (4096 x 1024: 8 experts 16.7 us for the pass, 7.7 at 6.56 TB/s; 64
+// 16 FMA (4096 x 1024: 8 experts 13.8 us for the pass, 7.7 at 6.56 TB/s; 64
 // experts 41 us, the reads' pipe at three quarters of its rate on the busiest
 // SMs; tiles of 8 x 8 and 8 x 4 on 128 columns leave one CTA an SM and took 40.5
 // there, but 44.5 us against 43.3 for 2048 x 4096 with 32 experts and 21 against
