@@ -67,7 +67,6 @@ struct Cfg {
   static constexpr int W_OFF = STAGES * STAGE;
   static constexpr int OUT_OFF = W_OFF + WB * kUnit;
   static constexpr int CTL_OFF = OUT_OFF + UNITS * kUnit;
-  static constexpr int KB = NB == 3 ? 2 : NB;  // blocks of dz in dx: hi and mid suffice
 };
 static_assert(Cfg<1>::CTL_OFF == 14 * kUnit && Cfg<2>::CTL_OFF == 14 * kUnit &&
               Cfg<3>::CTL_OFF == 14 * kUnit, "one shared-memory size");
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 16 experts are 32 bytes of a 128-byte row.
           const uint64_t adesc = smem_desc_sw128(src + 2 * kUnit, 16, 1024);
 #pragma unroll
-          for (int b = 0; b < C::KB; ++b)
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               tc_mma_bf16(tmem + buf * 128,
