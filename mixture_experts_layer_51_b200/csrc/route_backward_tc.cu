@@ -327,10 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return bits;
     };
+    // Without dW_g nobody reads x, and nobody waits for `clean`: following the
+    // ring then would be a wait that the ring could overtake.
     const bool scrub = p.mask && p.want_dw;
     uint32_t bits = scrub ? padding(0) : 0;
-    for (int i = 0; p.mask && i < ntiles; ++i) {
-      const uint32_t next = scrub && i + 1 < ntiles ? padding(i + 1) : 0;
+    for (int i = 0; scrub && i < ntiles; ++i) {
+      const uint32_t next = i + 1 < ntiles ? padding(i + 1) : 0;
       if (!__all_sync(0xffffffffu, !c.abort_flag && mbar_wait(smem_u32(&c.full[stage]), phase))) {
         give_up(p, c, kErrTimeoutMma);
         break;

@@ -64,3 +64,25 @@ def test_dx_keeps_dz_to_24_bits(E):
     tol = (2 * 2 + 1 + 1) * U32 * np.abs(np64(part)) + 2.0 ** -8 * np.abs(want)
     err = np.abs(np64(got["dx"]) - want)
     assert np.all(err <= tol), (err / tol).max()
+
+
+# ---------------------------------------------------------------- masks, waits
+@pytest.mark.parametrize("E", [8, 30, 64])
+@pytest.mark.parametrize("outputs", [("dx",), ("dx", "dbias")])
+def test_dx_of_a_padded_batch_without_dwg(E, outputs):
+    """Many tiles a range, with nobody to zero x for: the bits of the whole
+    call, and no wait that ran out."""
+    T, d = 20000, 2056
+    g = _gen(E)
+    a = _one_gate(g, T, E)
+    a.update(mask=torch.rand(T, generator=g, device=DEV) > 0.3,
+             dx_acc=_randn(g, T, d, dtype=torch.bfloat16))
+    x, Wg = (_randn(g, *s, dtype=torch.bfloat16) for s in ((T, d), (d, E)))
+    want = M.moe_route_backward(x, Wg, **a)
+    need = M.moe_route_backward_workspace_bytes(T, d, E, torch.bfloat16)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    for _ in range(5):
+        got = M.moe_route_backward(x, Wg, outputs=outputs, ws=ws, **a)
+        assert int(ws[:4].view(torch.int32)) == 0
+        for name in outputs:
+            assert torch.equal(got[name], want[name]), name
