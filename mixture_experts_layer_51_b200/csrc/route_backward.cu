@@ -103,21 +103,32 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
 }
 
 // v = hi + mid + lo, each with a bf16's eight significant bits (in the upper
-// half of its fp32 pattern): the nearest, then the nearest of what is left,
-// whose rest is exact.  Infinities and NaN stay in hi.
+// half of its fp32 pattern).  Each term is cut from just below what is left, so
+// that the next has something to hold: every term of a value other than zero
+// has that value's sign and is not zero, and an infinity in x or W_g times the
+// three adds up to what it gives with v (with terms of zero or of both signs,
+// NaN).  Infinities and NaN are all three terms.  Exact down to 2^-100; further
+// down a term may be too small for bf16 and is its least value then, 2^-133.
 struct Terms {
-  uint32_t hi, mid;
-  float lo;
+  uint32_t hi, mid, lo;
 };
 __device__ __forceinline__ Terms split(float v) {
-  constexpr uint32_t kExp = 0x7f800000u;
-  const uint32_t u = __float_as_uint(v), up = u + 0x8000u;
-  const bool finite = (u & kExp) != kExp;
-  Terms t;  // next to the largest values, hi is cut instead of rounded up
-  t.hi = (finite && (up & kExp) != kExp ? up : u) & 0xffff0000u;
-  const float rest = finite ? v - __uint_as_float(t.hi) : 0.f;
-  t.mid = (__float_as_uint(rest) + 0x8000u) & 0xffff0000u;
-  t.lo = rest - __uint_as_float(t.mid);
+  const uint32_t u = __float_as_uint(v), size = u & 0x7fffffffu;
+  if (size == 0 || size >= 0x7f800000u) {
+    const uint32_t same = size > 0x7f800000u ? u | 0x00400000u : u;  // NaN in the upper half
+    return {same, same, same};
+  }
+  const uint32_t least = (u & 0x80000000u) | 0x00010000u;
+  Terms t;
+  t.hi = (u - 1) & 0xffff0000u;
+  const float rest = v - __uint_as_float(t.hi);
+  t.mid = (__float_as_uint(rest) - 1) & 0xffff0000u;
+  t.lo = __float_as_uint(rest - __uint_as_float(t.mid));
+  if (size < 0x18000000u) {  // 2^-79: far above where a term runs out
+    if (!(t.hi & 0x7fff0000u)) t.hi = least;
+    if (!(t.mid & 0x7fff0000u)) t.mid = least;
+    if (!(t.lo & 0x7fff0000u)) t.lo = least;
+  }
   return t;
 }
 // The upper halves of two words, `a`'s below `b`'s.
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(kDzThreads, 4)
       const Terms x = split(v[0]), y = split(v[1]);
       hi2[i / 2] = upper_halves(x.hi, y.hi);
       mid2[i / 2] = upper_halves(x.mid, y.mid);
-      lo2[i / 2] = upper_halves(__float_as_uint(x.lo), __float_as_uint(y.lo));
+      lo2[i / 2] = upper_halves(x.lo, y.lo);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)

@@ -86,3 +86,142 @@ def test_dx_of_a_padded_batch_without_dwg(E, outputs):
         assert int(ws[:4].view(torch.int32)) == 0
         for name in outputs:
             assert torch.equal(got[name], want[name]), name
+
+
+# ------------------------------------------------------------------ infinities
+# Tokens and type: the one-launch kernel, the tensor cores, fp32 products.
+PATHS = [(40, torch.bfloat16), (300, torch.bfloat16), (300, torch.float32)]
+PIDS = ["small", "tensor", "fp32"]
+INF, NAN = float("inf"), float("nan")
+
+
+def _same_kind(got, want):
+    """NaN where the formula gives NaN, infinities of its signs where it gives
+    those, and finite values elsewhere."""
+    got = np64(got)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    odd = np.isinf(want)
+    assert np.array_equal(got[odd], want[odd])
+    assert np.isfinite(got[np.isfinite(want)]).all()
+
+
+@pytest.mark.parametrize("T,dtype", PATHS, ids=PIDS)
+@pytest.mark.parametrize("E", LAYOUTS)
+def test_infinities_give_what_fp32_products_give(E, T, dtype):
+    """Infinities and NaN in x and W_g at counted tokens, with a gradient at
+    every expert: those of the formula, and the other elements keep their
+    bits."""
+    d = 72
+    g = _gen(T + E)
+    z = _randn(g, T, E)
+    p = torch.softmax(z, 1)
+    idx = torch.topk(z, 2, 1).indices.int().contiguous()
+    a = dict(idx=idx, gate=p.gather(1, idx.long()).contiguous(), dgate=_randn(g, T, 2),
+             scores=p.t().contiguous(), gating="softmax_topk")
+    x, Wg = _randn(g, T, d, dtype=dtype), _randn(g, d, E, dtype=dtype)
+    plain = M.moe_route_backward(x, Wg, **a)
+    dz = oracle.router_dlogits(T, E, idx.cpu().numpy(), np64(a["gate"]), np64(a["dgate"]),
+                               np64(a["scores"]), gating="softmax_topk")
+    x[5, 3], x[9, 7], x[11, 20], x[12, 20], x[30, 71], x[31, 64] = INF, -INF, INF, -INF, NAN, INF
+    Wg[4, 0], Wg[6, 1], Wg[8, 0], Wg[8, 1], Wg[70, E - 1], Wg[71, 0] = INF, -INF, INF, -INF, NAN, INF
+    # With two experts and both taken dz may come out as zero or of either
+    # sign; the formula's own is what counts only where it is no rounding.
+    clear = np.abs(dz) > 1e-5 * np.abs(dz).max()
+    rows = [5, 9, 11, 12, 30, 31]
+    with np.errstate(invalid="ignore"):
+        dx, dWg, _ = oracle.route_backward(np64(x), np64(Wg), dz)
+    got = M.moe_route_backward(x, Wg, **a)
+    use = clear[rows].all(0)  # experts whose dz at those tokens has a sure sign
+    _same_kind(got["dWg"][:, torch.from_numpy(use)], dWg[:, use])
+    sure = clear.all(1)
+    assert use.any() and sure.any()
+    _same_kind(got["dx"][torch.from_numpy(sure)], dx[sure])
+    cols = torch.ones(d, dtype=torch.bool)
+    cols[[3, 7, 20, 71, 64]] = False
+    assert torch.equal(got["dWg"][cols], plain["dWg"][cols])
+    cols[:] = True
+    cols[[4, 6, 8, 70, 71]] = False
+    assert torch.equal(got["dx"][:, cols], plain["dx"][:, cols])
+
+
+@pytest.mark.parametrize("T,dtype", PATHS, ids=PIDS)
+@pytest.mark.parametrize("E", LAYOUTS)
+@pytest.mark.parametrize("v", [0.5, -1.0, 1.0 + 2.0 ** -23, 3e38, 1e-20, -1e-33, 1e-36, 1e-39, INF])
+def test_an_infinity_times_one_gradient(v, E, T, dtype):
+    """One expert of one token has a gradient, of few bits, many, or next to
+    the ends of the range: inf times it is inf, times the zeros NaN."""
+    d = 64
+    g = _gen(E)
+    x, Wg = _randn(g, T, d, dtype=dtype), _randn(g, d, E, dtype=dtype)
+    a = dict(idx=torch.full((T, 1), E // 2, device=DEV).int(), gate=torch.zeros((T, 1), device=DEV),
+             dgate=torch.zeros((T, 1), device=DEV), scores=torch.zeros((E, T), device=DEV),
+             gating="softmax_topk")
+    a["gate"][7], a["dgate"][7] = 1.0, v
+    x[7, 9], Wg[33, E // 2] = -INF, INF
+    got = M.moe_route_backward(x, Wg, **a, outputs=("dx", "dWg"))
+    # An infinite gate gradient is NaN at every expert of the token already:
+    # dz_e = [e = idx] g dg - p_e sum g dg, and p_e = 0 times infinity is NaN.
+    sign = NAN if v == INF else 1.0 if v > 0 else -1.0
+    want = np.full(E, NAN)
+    want[E // 2] = -sign * INF
+    assert np.array_equal(np64(got["dWg"][9]), want, equal_nan=True)
+    assert np.array_equal(np64(got["dx"][7, 33]), sign * INF, equal_nan=True)
+    assert got["dx"][8, 33].isnan()
+
+
+@pytest.mark.parametrize("T,dtype", PATHS, ids=PIDS)
+@pytest.mark.parametrize("E", LAYOUTS)
+@pytest.mark.parametrize("v", [1.0, 1.0 + 2.0 ** -23, 3.0e38, 3.4e38, -3.4e38, 1e-29, 1e-31, 1e-39,
+                               INF, -INF, NAN])
+def test_a_gradient_at_the_ends_of_the_range(v, E, T, dtype):
+    """As far as dz itself goes, in every layout of its terms: three terms of
+    one sign hold every value down to 2^-100, and the smaller ones to three
+    times bf16's least value."""
+    d = 64
+    x = torch.zeros((T, d), dtype=dtype, device=DEV)
+    x[7, 3] = 1.0
+    Wg = torch.zeros((d, E), dtype=dtype, device=DEV)
+    Wg[:, E - 1] = 0.5
+    a = dict(idx=torch.full((T, 1), E - 1, device=DEV).int(), gate=torch.zeros((T, 1), device=DEV),
+             dgate=torch.zeros((T, 1), device=DEV), scores=torch.zeros((E, T), device=DEV),
+             gating="softmax_topk")
+    a["gate"][7], a["dgate"][7] = 1.0, v
+    got = M.moe_route_backward(x, Wg, **a)
+    dx, dWg = np64(got["dx"]), np64(got["dWg"])
+    v = float(a["dgate"][7])  # in fp32
+    if not np.isfinite(v):  # p_e = 0 times the sum of g dg, infinite or NaN, is NaN
+        assert np.isnan(dWg[3]).all() and np.isnan(dx[7]).all()
+        return
+    # two additions, each off by at most a step; the least terms
+    tol = 4 * U32 * abs(v) + 3 * 2.0 ** -133
+    assert abs(dWg[3, E - 1] - v) <= tol and abs(float(got["dbias"][E - 1]) - v) <= 2.0 ** -149
+    # half the smallest numbers of the output's type more
+    u = torch.finfo(dtype).eps / 2
+    assert np.all(np.abs(dx[7] - v / 2) <= tol + u * abs(v) / 2 + 2.0 ** -134)
+    assert not np.delete(dx, 7, 0).any()
+
+
+@pytest.mark.parametrize("T,dtype", PATHS, ids=PIDS)
+@pytest.mark.parametrize("E", LAYOUTS)
+def test_an_infinite_gradient_of_the_loss(E, T, dtype):
+    """dz of both infinities at one token: each expert's in dW_g, NaN in the
+    sums over the experts (infinities of both signs)."""
+    d = 64
+    g = _gen(T * E)
+    scores = torch.zeros((E, T), device=DEV)
+    scores[:, 7] = torch.softmax(_randn(g, E), 0)
+    counts = torch.zeros(E, dtype=torch.int32, device=DEV)
+    counts[0] = T  # f = (1, 0, ...): f_e - sum f p is 1 - p_0 at the first expert, else -p_0
+    x, Wg = _randn(g, T, d, dtype=dtype), torch.ones((d, E), dtype=dtype, device=DEV)
+    x[7] = x[7].abs() + 1
+    tokens = torch.tensor([T], dtype=torch.int32, device=DEV)
+    mask = torch.arange(T, device=DEV) == 7  # the other tokens' p of 0 times infinity is NaN
+    got = M.moe_route_backward(x, Wg, torch.zeros((T, 1), dtype=torch.int32, device=DEV),
+                               scores=scores, counts=counts, tokens=tokens, coef=1.0,
+                               dloss=torch.tensor([INF], device=DEV), mask=mask)
+    want = np.full(E, -INF)
+    want[0] = INF
+    assert np.array_equal(np64(got["dWg"]), np.broadcast_to(want, (d, E)))
+    assert np.array_equal(np64(got["dbias"]), want)
+    dx = np64(got["dx"])
+    assert np.isnan(dx[7]).all() and not np.delete(dx, 7, 0).any()
