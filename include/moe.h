@@ -560,7 +560,11 @@ moe_status moe_balance_loss(const float* scores, const int32_t* idx, const uint8
  *   dx.  N == 0 adds nothing from the loss; T == 0 gives dWg = dbias = 0.
  *   ws: at least moe_route_backward_workspace_bytes(T, d, E, dtype).  With
  *   T > 0 its first int32 is an error word, written by every call: 0, or the
- *   bits of a kernel that gave up on a bounded wait (dWg is NaN then). */
+ *   bits of a kernel that gave up on a bounded wait.  The blocks of dx (up to
+ *   128 columns of a range of tokens) that it did not finish are NaN then, in
+ *   place of dx_acc too, and so are dWg's columns of these blocks or, where
+ *   many ranges are added up by a launch of their own, all of dWg; the rest
+ *   and dbias are right. */
 size_t moe_route_backward_workspace_bytes(int32_t T, int32_t d, int32_t E, moe_dtype dtype);
 moe_status moe_route_backward(const void* x, const void* Wg, const float* scores,
                               const int32_t* idx, const float* gate, const float* dgate,

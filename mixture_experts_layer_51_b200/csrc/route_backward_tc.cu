@@ -19,7 +19,7 @@
 // anything, and 0 * NaN is NaN), 4-11 epilogue, in two groups that take the
 // 64-column halves of the tiles in turn.  Every wait is bounded; a time-out
 // raises the workspace's error word and the CTA leaves after its copies and
-// MMAs have landed.
+// MMAs have landed, its block of dx (and its columns of dW_g) filled with NaN.
 //
 // Measured on one B200, all launches of the backward pass (floors at
 // 6.56 TB/s in brackets): 8192 x 4096, 8 experts, with dx_acc 39.8 us (30.8),
@@ -34,6 +34,9 @@
 
 #include <cudaTypedefs.h>
 
+#include <stdlib.h>
+
+#include <atomic>
 #include <mutex>
 
 #include "route_backward.cuh"
@@ -75,7 +78,7 @@ struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
   uint64_t tfull[2], tempty[2];                    // dx accumulators
   uint64_t uready[kMaxUnits], ustaged[kMaxUnits];  // staging units
-  uint64_t dwfull, dwempty, wready, drain;
+  uint64_t dwfull, dwempty, wready, drain, never;
   uint32_t tmem_base;
   uint32_t last;  // this CTA finished last of its column block
   volatile int abort_flag;
@@ -84,9 +87,11 @@ struct Ctl {
 struct Params {
   const __nv_bfloat16* Wg;
   const uint8_t* mask;
+  __nv_bfloat16* dx;  // what a CTA that gave up marks; the results leave by TMA
   RouteSums sums;
   int T, d, E, stride, cols, ranges, tiles;
   int want_dx, want_dw, add;
+  int debug_stall;  // 1: CTA 0's MMA issuer first waits on a barrier nobody arms (tests only)
 };
 
 __device__ __forceinline__ void give_up(const Params& p, Ctl& c, int code) {
@@ -155,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&c.dwempty), kEpilogue / 32);
     mbar_init(smem_u32(&c.wready), kEpilogue);
     mbar_init(smem_u32(&c.drain), 1);
+    mbar_init(smem_u32(&c.never), 1);
     c.abort_flag = 0;
     fence_mbar_init();
     fence_async_shared();
@@ -221,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_dx = idesc_bf16_f32(128, 128, false, false);
       const uint64_t wdesc = smem_desc_sw128(base + C::W_OFF, 16, 1024);
       bool ok = mbar_wait(smem_u32(&c.wready), 0);
+      if (p.debug_stall && blockIdx.x == 0) ok = mbar_wait(smem_u32(&c.never), 0);
       if (!ok) give_up(p, c, kErrTimeoutMma);
       int stage = 0, flushed = 0;
       uint32_t phase = 0;
@@ -542,6 +549,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (c.abort_flag && p.want_dx) {
+    // Which tiles were stored is not known here: none of them counts.
+    const int chunks = min(kRbTcCols, p.d - c0) / 8;  // columns come in eights
+    const int rows = min(ntiles * kRbTcTokens, p.T - tile0 * kRbTcTokens);
+    __nv_bfloat16* to = p.dx + static_cast<int64_t>(tile0) * kRbTcTokens * p.d + c0;
+    const uint4 nan = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+    for (int64_t i = tid; i < static_cast<int64_t>(rows) * chunks; i += kThreads)
+      *reinterpret_cast<uint4*>(to + i / chunks * p.d + i % chunks * 8) = nan;
+  }
+}
+
+// Failure-detection tests: MOE_DEBUG_STALL_ROUTE=N lets one CTA of the next N
+// launches run out of its waits (read once per process).
+int take_debug_stall() {
+  static std::atomic<int> budget{[] {
+    const char* v = getenv("MOE_DEBUG_STALL_ROUTE");
+    return v ? atoi(v) : 0;
+  }()};
+  int cur = budget.load();
+  while (cur > 0 && !budget.compare_exchange_weak(cur, cur - 1)) {
+  }
+  return cur > 0 ? 1 : 0;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -586,6 +615,7 @@ cudaError_t launch_route_products_tc(const RouteBackwardArgs& a, const RouteBack
     return cudaErrorInvalidValue;
   Params k{static_cast<const __nv_bfloat16*>(a.Wg),
            a.mask,
+           static_cast<__nv_bfloat16*>(a.dx),
            sums,
            a.T,
            a.d,
@@ -596,7 +626,8 @@ cudaError_t launch_route_products_tc(const RouteBackwardArgs& a, const RouteBack
            p.tiles,
            a.dx != nullptr,
            a.dWg != nullptr,
-           a.dx && a.dx_acc};
+           a.dx && a.dx_acc,
+           take_debug_stall()};
   auto go = [&](auto kern) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;

@@ -661,7 +661,8 @@ class MoELayer:
         balance loss [1] weighted by coef (mask: see moe_balance_loss), and
         ``step``, the dict of intermediates that backward_combine and
         backward_router read (xp, h, o, offsets and kept_counts among them,
-        for a backward pass of the experts).  x and rng are held, not copied:
+        for a backward pass of the experts; dev_error is the experts' error
+        word, as moe_grouped_ffn returned it).  x and rng are held, not copied:
         neither may change before the backward pass."""
         _tensor(x, "x", self.dtype, (x.shape[0], self.d), self.device.index)
         idx, gate, _ = moe_route(x, self.Wg, self.bias, self.k, gating=self.gating,
@@ -693,16 +694,24 @@ class MoELayer:
         """The router's gradients after backward_combine, as a dict: through
         the gates and the balance loss (dloss [1]: its gradient, None for 1).
         dxp: the gradient of the permuted tokens step["xp"] from the experts'
-        own backward pass; dx then holds both."""
+        own backward pass; dx then holds both.  step["router_error"] is the
+        kernels' error word (int32 [1] on the device, 0 unless one gave up on a
+        bounded wait; dx and dWg hold NaN then)."""
         dx_acc = None
         if dxp is not None and "dx" in outputs:
             _tensor(dxp, "dxp", self.dtype, step["xp"].shape, self.device.index)
             dx_acc = moe_unpermute_combine(dxp, step["pos"], torch.ones_like(step["gate"]),
                                            step["x"].dtype)
+        T = step["x"].shape[0]
+        ws = _workspace(None, moe_route_backward_workspace_bytes(T, self.d, self.E, self.dtype),
+                        self.device, None)
+        step["router_error"] = ws[:4].view(torch.int32)
+        if T == 0:  # no kernel runs
+            step["router_error"].zero_()
         return moe_route_backward(step["x"], self.Wg, step["idx"], step["gate"], step["dgate"],
                                   step["scores"], step["balance_counts"], step["tokens"],
                                   step["coef"], dloss, step["mask"], self.gating, self.gate_scale,
-                                  dx_acc=dx_acc, dx=dx_acc, outputs=outputs)
+                                  dx_acc=dx_acc, dx=dx_acc, outputs=outputs, ws=ws)
 
     def graph(self, x, y=None):
         """A ForwardGraph of this layer on x (and y, allocated if None)."""
@@ -830,7 +839,9 @@ def moe_route_backward(x, Wg, idx, gate=None, dgate=None, scores=None, counts=No
     loss; None for 1) -- either or both.  scores [E, T] serve the loss and
     the softmax-then-TopK gates.  dx is added to dx_acc where that is given
     (dx may be dx_acc itself).  ``outputs`` names the gradients to compute;
-    returns them as a dict (dx in the layer dtype, the others fp32)."""
+    returns them as a dict (dx in the layer dtype, the others fp32).  A kernel
+    that gave up on a bounded wait leaves NaN in dx and dWg, and its bits in
+    the first int32 of ws (which the caller has to pass to read it)."""
     T, d = x.shape
     E = Wg.shape[1]
     k = idx.shape[1]

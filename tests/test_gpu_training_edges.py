@@ -7,6 +7,11 @@ a step of fp32, 2^-8 of bf16.  A sum in tensor memory does not round to
 nearest: each of its steps is off by at most a whole step, 2 u.
 """
 
+import os
+import subprocess
+import sys
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -18,6 +23,7 @@ pytestmark = pytest.mark.gpu
 
 U32 = 2.0 ** -24
 DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 # Experts in each layout of dz's bf16 terms (one, two and three 64-wide
 # blocks), at the ends of each.
@@ -225,3 +231,81 @@ def test_an_infinite_gradient_of_the_loss(E, T, dtype):
     assert np.array_equal(np64(got["dbias"]), want)
     dx = np64(got["dx"])
     assert np.isnan(dx[7]).all() and not np.delete(dx, 7, 0).any()
+
+
+# ------------------------------------------------------- waits that run out
+STALLED = textwrap.dedent("""
+    import sys, torch
+    sys.path.insert(0, {root!r})
+    from mixture_experts_layer_51_b200 import moe as M
+    ERR_TIMEOUT_MMA = 1 << 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda")
+    # T, d, E, whether a launch of its own adds the ranges, mask, outputs
+    CASES = [(600, 200, 8, False, False, ("dx", "dWg", "dbias")),
+             (2000, 392, 64, False, True, ("dx", "dWg", "dbias")),
+             (20000, 136, 30, True, True, ("dx", "dWg", "dbias")),
+             (900, 264, 30, False, True, ("dx",)),
+             (700, 264, 43, False, False, ("dx", "dbias")),
+             (700, 264, 43, False, True, ("dWg",))]
+    calls = []
+    for T, d, E, _, masked, outputs in CASES:
+        p = torch.softmax(rand(T, E), 1)
+        idx = torch.topk(p, 2, 1).indices.int().contiguous()
+        need = M.moe_route_backward_workspace_bytes(T, d, E, torch.bfloat16)
+        calls.append(dict(
+            x=rand(T, d).bfloat16(), Wg=rand(d, E).bfloat16(), idx=idx,
+            gate=p.gather(1, idx.long()).contiguous(), dgate=rand(T, 2),
+            scores=p.t().contiguous(), gating="softmax_topk", outputs=outputs,
+            mask=torch.arange(T, device="cuda") % 3 > 0 if masked else None,
+            dx_acc=rand(T, d).bfloat16() if "dx" in outputs else None,
+            ws=torch.empty(need, dtype=torch.uint8, device="cuda")))
+    bads, words = [], []
+    for a in calls:  # the launches that stall, dx in place
+        buf = a["dx_acc"].clone() if a["dx_acc"] is not None else None
+        bads.append(M.moe_route_backward(**dict(a, dx_acc=buf, dx=buf)))
+        words.append(int(a["ws"][:4].view(torch.int32)))
+    for (T, d, E, many, _, outputs), a, bad, word in zip(CASES, calls, bads, words):
+        assert word & ERR_TIMEOUT_MMA, word
+        good = M.moe_route_backward(**a)
+        assert int(a["ws"][:4].view(torch.int32)) == 0
+        assert all(torch.isfinite(good[n].float()).all() for n in outputs)
+        if "dx" in outputs:
+            lost = bad["dx"].isnan()
+            rows = int(lost.any(1).sum())
+            assert 0 < rows and (rows == T or rows % 128 == 0), rows
+            assert lost[:rows, :128].all() and not lost[rows:].any() and not lost[:, 128:].any()
+            assert torch.equal(bad["dx"][~lost], good["dx"][~lost])
+        if "dWg" in outputs:
+            lost = bad["dWg"].isnan()
+            assert lost[:128].all()
+            assert lost[128:].all() if many else not lost[128:].any()
+            assert torch.equal(bad["dWg"][~lost], good["dWg"][~lost])
+        if "dbias" in outputs:
+            assert torch.equal(bad["dbias"], good["dbias"])
+        print("REPORTED")
+""")
+
+
+def test_a_wait_that_runs_out_marks_what_it_left():
+    """One CTA of the tensor-core kernel runs out of its bounded waits: the
+    error word says so, its block of dx and its columns of dW_g are NaN, the
+    rest is right, and so is the next call of the same."""
+    env = dict(os.environ, MOE_DEBUG_STALL_ROUTE="6")
+    r = subprocess.run([sys.executable, "-c", STALLED.format(root=ROOT)], env=env,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr[-3000:]
+    assert r.stdout.count("REPORTED") == 6
+
+
+def test_a_step_keeps_the_router_error_word():
+    from mixture_experts_layer_51_b200.workloads import Workload, make_inputs
+    w = Workload("t", T=300, d=64, E=4, k=2, H=64, act="swiglu", dtype="bf16", cf=0.0, seed=9)
+    t = make_inputs(w, DEV)
+    layer = M.MoELayer(t["Wg"], t["bias"], t["W1"], t["W3"], t["W2"], w.k, w.cf, w.act)
+    for x in (t["x"], t["x"][:7], t["x"][:0]):
+        y, _, step = layer.forward_train(x, coef=0.1)
+        layer.backward_combine(step, torch.ones_like(y))
+        layer.backward_router(step)
+        assert step["router_error"].dtype == torch.int32 and int(step["router_error"]) == 0
