@@ -34,6 +34,8 @@ namespace {
 constexpr int kCdWarps = 8;
 
 // Eight consecutive elements: their bytes, as loaded and stored, and in fp32.
+// load() takes the read-only path, for what nobody writes during the kernel;
+// load_plain() is for the residual, which y may be.
 template <bool BF16>
 struct Chunk;
 template <>
@@ -42,6 +44,9 @@ struct Chunk<true> {
   uint4 v;
   __device__ __forceinline__ void load(const char* p) {
     v = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void load_plain(const char* p) {
+    v = *reinterpret_cast<const uint4*>(p);
   }
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
   // Elements 2 i and 2 i + 1 stay where the low and high half of m[i] are all
@@ -70,6 +75,10 @@ struct Chunk<false> {
   __device__ __forceinline__ void load(const char* p) {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void load_plain(const char* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void mask(const uint32_t (&m)[4]) {
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(kCdWarps * 32)
           v[j][h].zero();
       }
       if (residual && in)
-        res[h].load(rest + at_c + h * L * B);
+        res[h].load_plain(rest + at_c + h * L * B);
       else
         res[h].zero();
     }

@@ -309,3 +309,25 @@ def test_a_step_keeps_the_router_error_word():
         layer.backward_combine(step, torch.ones_like(y))
         layer.backward_router(step)
         assert step["router_error"].dtype == torch.int32 and int(step["router_error"]) == 0
+
+
+# ------------------------------------------------------- the residual in place
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T,d,k", [(4000, 64, 2), (3001, 128, 4), (2000, 2056, 2), (300, 4104, 8),
+                                   (1, 136, 1)])
+def test_the_combine_onto_its_residual_again_and_again(T, d, k, dtype):
+    """y is the residual, call after call with nothing in between: the bits of
+    the same calls into buffers of their own."""
+    g = _gen(T + d + k)
+    rows = T * k
+    o = _randn(g, rows, d, dtype=dtype)
+    pos = torch.randperm(rows, generator=g, device=DEV).int().view(T, k)
+    gate = torch.rand((T, k), generator=g, device=DEV)
+    rng = torch.tensor([11, 12], device=DEV)
+    start = _randn(g, T, d, dtype=dtype)
+    buf, want = start.clone(), start
+    for _ in range(6):
+        M.moe_combine_dropout(o, pos, gate, 0.3, rng, residual=buf, y=buf)
+    for _ in range(6):
+        want = M.moe_combine_dropout(o, pos, gate, 0.3, rng, residual=want)
+    assert torch.equal(buf, want)
