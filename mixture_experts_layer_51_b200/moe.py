@@ -616,6 +616,19 @@ class ForwardGraph:
             pass
 
 
+def _on_layer_device(method):
+    """A method whose calls run with the layer's device current: the library
+    launches on the current device, and a stream belongs to one."""
+    @functools.wraps(method)
+    def call(self, *args, **kwargs):
+        index = self.device.index
+        if index is None or _current_device() == index:
+            return method(self, *args, **kwargs)
+        with torch.cuda.device(index):
+            return method(self, *args, **kwargs)
+    return call
+
+
 class MoELayer:
     """Weights plus a persistent workspace for repeated forwards on one
     device (no allocation per call)."""
@@ -655,12 +668,13 @@ class MoELayer:
                            stream=stream, gating=self.gating, gate_scale=self.gate_scale,
                            priority=self.priority)
 
+    @_on_layer_device
     def forward_train(self, x, coef=0.0, mask=None, residual=None, p=0.0, rng=None):
         """One forward pass that a backward pass can follow, on the current
-        stream: (y, loss, step) with y = residual + dropout_p(layer(x)), the
-        balance loss [1] weighted by coef (mask: see moe_balance_loss), and
-        ``step``, the dict of intermediates that backward_combine and
-        backward_router read (xp, h, o, offsets and kept_counts among them,
+        stream of the layer's device: (y, loss, step) with y = residual +
+        dropout_p(layer(x)), the balance loss [1] weighted by coef (mask: see
+        moe_balance_loss), and ``step``, the dict of intermediates that
+        backward_combine and backward_router read (xp, h, o, offsets and kept_counts among them,
         for a backward pass of the experts; dev_error is the experts' error
         word, as moe_grouped_ffn returned it).  x and rng are held, not copied:
         neither may change before the backward pass."""
@@ -682,6 +696,7 @@ class MoELayer:
                     dev_error=dev_error, **perm)
         return y, balance["loss"], step
 
+    @_on_layer_device
     def backward_combine(self, step, dy, d_o=None):
         """d_o, the gradient of the expert outputs step["o"] (kept rows only);
         the gates' gradient is left in step["dgate"]."""
@@ -690,6 +705,7 @@ class MoELayer:
                                                           d_o=d_o)
         return d_o
 
+    @_on_layer_device
     def backward_router(self, step, dloss=None, dxp=None, outputs=("dx", "dWg", "dbias")):
         """The router's gradients after backward_combine, as a dict: through
         the gates and the balance loss (dloss [1]: its gradient, None for 1).
