@@ -676,9 +676,13 @@ class MoELayer:
         moe_balance_loss), and ``step``, the dict of intermediates that
         backward_combine and backward_router read (xp, h, o, offsets and kept_counts among them,
         for a backward pass of the experts; dev_error is the experts' error
-        word, as moe_grouped_ffn returned it).  x and rng are held, not copied:
-        neither may change before the backward pass."""
+        word, as moe_grouped_ffn returned it).  x, mask and rng are held, not
+        copied: none may change before the backward pass.  Nothing is recorded
+        for autograd: tensors that require a gradient are refused outside
+        torch.no_grad()."""
         _tensor(x, "x", self.dtype, (x.shape[0], self.d), self.device.index)
+        for name in ("Wg", "bias", "W1", "W3", "W2"):
+            _refuse_autograd(getattr(self, name), name)
         idx, gate, _ = moe_route(x, self.Wg, self.bias, self.k, gating=self.gating,
                                  gate_scale=self.gate_scale)
         scores = moe_expert_choice_route(x, self.Wg, self.bias)
@@ -739,10 +743,12 @@ class MoELayer:
 def _tensor(t, name, dtype, shape, index):
     """The address of an argument that the kernels will read or write: its
     type, shape, CUDA device (by index) and dense layout are checked here,
-    because a raw pointer carries none of them.  None passes as NULL."""
+    because a raw pointer carries none of them, and that autograd does not
+    watch it, because these calls record nothing.  None passes as NULL."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+            and not t.requires_grad):
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
@@ -750,7 +756,18 @@ def _tensor(t, name, dtype, shape, index):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    raise ValueError(f"{name} is not contiguous")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    _refuse_autograd(t, name)
+    return t.data_ptr()
+
+
+def _refuse_autograd(t, name):
+    """The gradients of these calls are calls of their own: a tensor of a live
+    autograd graph would come back cut off from it, without a word."""
+    if t is not None and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this call does not record: pass "
+                         f"{name}.detach(), or call under torch.no_grad()")
 
 
 def _mask(mask, T, index):

@@ -331,3 +331,33 @@ def test_the_combine_onto_its_residual_again_and_again(T, d, k, dtype):
     for _ in range(6):
         want = M.moe_combine_dropout(o, pos, gate, 0.3, rng, residual=want)
     assert torch.equal(buf, want)
+
+
+# ------------------------------------------------------------------- autograd
+def test_calls_refuse_tensors_that_autograd_watches():
+    """Every entry point, for any of its tensors; under no_grad they run."""
+    from mixture_experts_layer_51_b200.workloads import Workload, make_inputs
+    w = Workload("t", T=300, d=64, E=4, k=2, H=64, act="swiglu", dtype="bf16", cf=0.0, seed=9)
+    t = make_inputs(w, DEV)
+    layer = M.MoELayer(t["Wg"], t["bias"], t["W1"], t["W3"], t["W2"], w.k, w.cf, w.act)
+    x = t["x"]
+    y, _, s = layer.forward_train(x, coef=0.1)
+    watched = x.clone().requires_grad_()
+    o, gate, scores = (s[n].clone().requires_grad_() for n in ("o", "gate", "scores"))
+    calls = [
+        lambda: layer.forward_train(watched),
+        lambda: layer.forward_train(watched * 1),
+        lambda: layer.forward_train(x, residual=watched),
+        lambda: layer.backward_combine(s, watched),
+        lambda: M.moe_balance_loss(scores, s["idx"], 0.1)["loss"],
+        lambda: M.moe_combine_dropout(o, s["pos"], s["gate"]),
+        lambda: M.moe_combine_dropout(s["o"], s["pos"], gate),
+        lambda: M.moe_combine_dropout_backward(y, o, s["pos"], s["gate"]),
+        lambda: M.moe_route_backward(watched, layer.Wg, s["idx"], s["gate"], s["gate"]),
+        lambda: M.moe_route_backward(x, layer.Wg, s["idx"], s["gate"], gate),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+        with torch.no_grad():
+            call()

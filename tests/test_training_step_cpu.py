@@ -1,4 +1,5 @@
-"""The training step's host side, without a GPU: which device its calls run on."""
+"""The training step's host side, without a GPU: which device its calls run on,
+and what its checks of tensors refuse."""
 
 import pytest
 import torch
@@ -73,3 +74,27 @@ def test_the_device_is_put_back_after_an_error(step, monkeypatch):
     with pytest.raises(M.MoeError):
         layer.forward_train(torch.zeros(4, 16))
     assert now[0] == 0
+
+
+def test_a_tensor_that_autograd_watches_is_refused():
+    """... and passes where autograd does not record."""
+    w = torch.zeros(3, requires_grad=True)
+    with pytest.raises(ValueError, match="t requires a gradient"):
+        M._tensor(w, "t", torch.float32, (3,), -1)
+    with pytest.raises(ValueError, match="t requires a gradient"):
+        M._tensor(w * 2, "t", torch.float32, (3,), -1)
+    assert M._tensor(w.detach(), "t", torch.float32, (3,), -1) == w.data_ptr()
+    with torch.no_grad():
+        assert M._tensor(w, "t", torch.float32, (3,), -1) == w.data_ptr()
+
+
+@pytest.mark.parametrize("name", ["Wg", "W1", "W3", "W2"])
+def test_the_step_refuses_weights_that_autograd_watches(step, name):
+    layer, _, seen = step
+    setattr(layer, name, torch.nn.Parameter(getattr(layer, name)))
+    with pytest.raises(ValueError, match=f"{name} requires a gradient"):
+        layer.forward_train(torch.zeros(4, 16))
+    assert not seen
+    with torch.no_grad():
+        layer.forward_train(torch.zeros(4, 16))
+    assert seen
