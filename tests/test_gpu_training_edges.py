@@ -361,3 +361,87 @@ def test_calls_refuse_tensors_that_autograd_watches():
             call()
         with torch.no_grad():
             call()
+
+
+# ---------------------------------------------------- a batch split over ranks
+@pytest.mark.parametrize("T,d,E,k,dtype", [(1500, 136, 8, 2, torch.bfloat16),
+                                           (3001, 264, 64, 8, torch.bfloat16),
+                                           (1100, 72, 12, 3, torch.float32)])
+def test_two_parts_of_a_batch_with_summed_counts(T, d, E, k, dtype):
+    """counts, tokens and prob_sum of two parts add up to the whole batch's;
+    with the sums each part's dx is the whole's, bit for bit, and dW_g and
+    dbias add up to it."""
+    g = _gen(T)
+    z = _randn(g, T, E) + _randn(g, E)
+    scores, idx = torch.softmax(z, 1), torch.topk(z, k, 1).indices.int().contiguous()
+    x, Wg = _randn(g, T, d, dtype=dtype), _randn(g, d, E, dtype=dtype)
+    mask = torch.rand(T, generator=g, device=DEV) > 0.2
+    dloss = torch.tensor([float(T)], device=DEV)
+    parts = [slice(0, 2 * T // 5), slice(2 * T // 5, T)]
+
+    def balance(rows):
+        return M.moe_balance_loss(scores[rows].t().contiguous(), idx[rows], 0.2, mask=mask[rows])
+
+    def backward(rows, counts, tokens):
+        return M.moe_route_backward(x[rows], Wg, idx[rows], scores=scores[rows].t().contiguous(),
+                                    counts=counts, tokens=tokens, coef=0.2, dloss=dloss,
+                                    mask=mask[rows])
+    whole = balance(slice(0, T))
+    some = [balance(r) for r in parts]
+    sums = {n: some[0][n] + some[1][n] for n in ("counts", "tokens", "prob_sum")}
+    assert torch.equal(sums["counts"], whole["counts"])
+    assert torch.equal(sums["tokens"], whole["tokens"])
+    n = int(sums["tokens"])
+    loss = 0.2 * E * float((np64(sums["counts"]) / (n * k) * np64(sums["prob_sum"]) / n).sum())
+    assert abs(float(whole["loss"]) - loss) <= (2 * T + 4) * U32 * loss
+    want = backward(slice(0, T), whole["counts"], whole["tokens"])
+    got = [backward(r, sums["counts"], sums["tokens"]) for r in parts]
+    assert torch.equal(torch.cat([got[0]["dx"], got[1]["dx"]]), want["dx"])
+    dz = oracle.router_dlogits(T, E, idx=idx.cpu().numpy(), scores=np64(scores.t()),
+                               counts=np64(whole["counts"]), tokens=n, coef=0.2,
+                               dloss=float(T), mask=mask.cpu().numpy())
+    f = np64(whole["counts"]) / (n * k)
+    # dz by a difference of two sums, then T terms each way, the parts' sum
+    size = np.abs(dz) + 0.2 * E * np64(scores) * np.abs(np64(scores) @ f)[:, None] * 2
+    ax = np.abs(np64(x)) * mask.cpu().numpy()[:, None]
+    for name, tol in (("dWg", ax.T @ size), ("dbias", size.sum(0))):
+        err = np.abs(np64(got[0][name]) + np64(got[1][name]) - np64(want[name]))
+        assert np.all(err <= 2 * (T + E + 12) * U32 * tol), name
+
+
+# ----------------------------------------- one expert, nothing but padding
+BOTH = [torch.bfloat16, torch.float32]
+
+
+@pytest.mark.parametrize("dtype", BOTH, ids=["tensor", "fp32"])
+@pytest.mark.parametrize("gating", ["topk_softmax", "softmax_topk"])
+def test_one_expert_past_the_small_batches(gating, dtype):
+    """A router with one expert has nothing to learn: zeros, and dx_acc."""
+    T, d = 700, 136
+    g = _gen(1)
+    acc = _randn(g, T, d, dtype=dtype)
+    one = torch.ones((T, 1), device=DEV)
+    got = M.moe_route_backward(_randn(g, T, d, dtype=dtype), _randn(g, d, 1, dtype=dtype),
+                               torch.zeros((T, 1), device=DEV).int(), one, _randn(g, T, 1),
+                               one.t().contiguous(), torch.tensor([T], device=DEV).int(),
+                               torch.tensor([T], device=DEV).int(), coef=0.5, gating=gating,
+                               dx_acc=acc)
+    assert torch.equal(got["dx"], acc) and not got["dWg"].any() and not got["dbias"].any()
+
+
+@pytest.mark.parametrize("dtype", BOTH, ids=["tensor", "fp32"])
+@pytest.mark.parametrize("E", [8, 30, 64])
+def test_a_batch_of_padding_past_the_small_batches(E, dtype):
+    """The mask leaves no token: zeros and dx_acc, whatever the rest holds."""
+    T, d, k = 900, 264, 2
+    g = _gen(E)
+    mask = torch.zeros(T, dtype=torch.bool, device=DEV)
+    nan = lambda *s: torch.full(s, NAN, device=DEV)  # noqa: E731
+    idx = torch.full((T, k), 1 << 30, device=DEV).int()
+    bal = M.moe_balance_loss(nan(E, T), idx, 0.5, mask=mask)
+    assert float(bal["loss"]) == 0 and int(bal["tokens"]) == 0 and not bal["prob_sum"].any()
+    acc = _randn(g, T, d, dtype=dtype)
+    got = M.moe_route_backward(nan(T, d).to(dtype), _randn(g, d, E, dtype=dtype), idx, nan(T, k),
+                               nan(T, k), nan(E, T), bal["counts"], bal["tokens"], coef=0.5,
+                               mask=mask, gating="softmax_topk", dx_acc=acc)
+    assert torch.equal(got["dx"], acc) and not got["dWg"].any() and not got["dbias"].any()

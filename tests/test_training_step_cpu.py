@@ -98,3 +98,13 @@ def test_the_step_refuses_weights_that_autograd_watches(step, name):
     with torch.no_grad():
         layer.forward_train(torch.zeros(4, 16))
     assert seen
+
+
+def test_a_tensor_that_is_not_dense_is_refused():
+    """By its strides: type, shape and device (-1: not on a GPU) are right."""
+    t = torch.zeros(4, 3).t()
+    with pytest.raises(ValueError, match="t is not contiguous"):
+        M._tensor(t, "t", torch.float32, (3, 4), -1)
+    assert M._tensor(t.contiguous(), "t", torch.float32, (3, 4), -1) is not None
+    with pytest.raises(ValueError, match="t is on cpu, expected cuda:0"):
+        M._tensor(t, "t", torch.float32, (3, 4), 0)
