@@ -56,21 +56,36 @@ int pick_ranges(int cols, int tiles, int per_sm) {
 
 // The ranges of dW_g are added by the last CTA of a column block, or by a
 // launch over all SMs.  The launch is quicker on the GPU from about five
-// ranges on (16384 x 2048, 64 experts, 9 ranges: 40.0 us for the pass against
-// 42.1; 16384 x 1024, 8 experts, 18 ranges: 18.9 against 22.6; 16384 x 64, 64
-// experts, 128 ranges: 13.7 against 51; at four ranges both take 39.8 us), but
-// costs the host 2.3 us.  A call from Python takes the host about 16 us
-// without it, so passes that the GPU is through with in that time (x of less
-// than 16 MB) do without, as long as one CTA has no more than 20 to add
-// (2048 x 2048, 8 experts, 9 ranges: 11.0 us on the GPU with the launch and
-// 12.0 without).  At 16 MB a call takes as long either way, or less with the
-// launch, and the GPU is done earlier (4096 x 1024 fp32, 16 ranges, inputs not
-// in L2: 17.8 to 18.6 us a call with it and 18.3 without; from L2 13.8 and 16.7 on
-// the GPU; 8192 x 1024, 16 experts, 18 ranges: 18.2 and 18.9 a call, 14.1 and
-// 18.9 on the GPU).
+// ranges on (in a graph, with and without it: 16384 x 2048, 64 experts, 9
+// ranges, bf16 40.0 and 42.1 us; 1001 x 1032, 8 experts, 8 ranges, bf16 8.3 and
+// 9.8; 2048 x 1024, 8 experts, 16 ranges, fp32 9.5 and 11.6; 16384 x 64, 64
+// experts, 128 ranges, bf16 13.7 and 51; at four ranges both take as long), but
+// costs the host 2 us, and a call from Python takes the host about 16 us
+// without it.  So a pass that the GPU is through with in that time does without
+// (the first two shapes after the large one: 18.3 and 16.2 us a call, 18.3 and
+// 16.3), as long as one CTA has no more than 20 ranges to add.  How long the
+// GPU takes goes by x's bytes, and, with many experts, by the products
+// (us a call with the launch and without):
+//   bytes: fp32, 8 experts, 2048 x 2048 (16 MB) 18.1 and 16.2, 4096 x 1536 (24
+//   MB) 18.5 and 20.1; bf16, 16 experts, 6000 x 1024 (12 MB) 18.8 and 18.1, 8192
+//   x 1024 (16 MB) 18.6 and 19.7: even at about 14 MB, where a graph gains 2 to
+//   5 us already;
+//   products, fp32: 2048 x 1024, 16 experts (33 M) 18.2 and 16.4, 4096 x 768, 16
+//   experts (50 M) 18.4 and 21.8, 1001 x 1032, 64 experts (66 M) 18.3 and 22.3;
+//   bf16, which are quicker, with the ranges' sum the longer part: 1001 x 1032, 64
+//   experts (66 M) 18.4 and 16.4, 2048 x 1024, 64 experts (134 M) 18.6 and 18.4,
+//   4096 x 768, 64 experts (201 M) 18.7 and 20.1.
 constexpr int kFewRanges = 4;
 constexpr int kPassingRanges = 20;
-constexpr int64_t kSummingLaunchBytes = 16 << 20;
+constexpr int64_t kSummingBytes = 14 << 20;                          // of x
+constexpr int64_t kSummingFp32 = 42000000, kSummingBf16 = 112000000;  // T d E
+
+bool sum_by_launch(int ranges, int T, int d, int E, bool tc) {
+  const int64_t elements = static_cast<int64_t>(T) * d;
+  return ranges > kPassingRanges ||
+         (ranges > kFewRanges && (elements * (tc ? 2 : 4) >= kSummingBytes ||
+                                  elements * E >= (tc ? kSummingBf16 : kSummingFp32)));
+}
 
 RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   RouteBackwardPlan p{};
@@ -81,9 +96,7 @@ RouteBackwardPlan make_plan(int T, int d, int E, moe_dtype dtype) {
   p.cols = (d + cols - 1) / cols;
   p.tiles = (T + tile - 1) / tile;
   p.ranges = T > 0 ? pick_ranges(p.cols, p.tiles, tc ? 1 : 2) : 0;
-  p.many = p.ranges > kPassingRanges ||
-           (p.ranges > kFewRanges &&
-            static_cast<int64_t>(T) * d * (tc ? 2 : 4) >= kSummingLaunchBytes);
+  p.many = sum_by_launch(p.ranges, T, d, E, tc);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;

@@ -445,3 +445,17 @@ def test_a_batch_of_padding_past_the_small_batches(E, dtype):
                                nan(T, k), nan(E, T), bal["counts"], bal["tokens"], coef=0.5,
                                mask=mask, gating="softmax_topk", dx_acc=acc)
     assert torch.equal(got["dx"], acc) and not got["dWg"].any() and not got["dbias"].any()
+
+
+# ------------------------------------------ around the choice of who adds dW_g
+@pytest.mark.parametrize("T,d,E,dtype", [
+    (3400, 1024, 8, "fp32"), (3700, 1024, 8, "fp32"),    # by the bytes of x
+    (6800, 1024, 8, "bf16"), (7400, 1024, 8, "bf16"),
+    (1001, 1032, 40, "fp32"), (1001, 1032, 41, "fp32"),  # by the products
+    (1650, 1032, 64, "bf16"), (1700, 1032, 64, "bf16")])
+def test_route_backward_around_the_summing_launch(T, d, E, dtype):
+    from test_gpu_training import _check_route, _route_case
+    a = _route_case(T, d, E, 2, dtype, "softmax_topk", 1.0, True, True, "some", True)
+    got, again = M.moe_route_backward(**a), M.moe_route_backward(**a)
+    _check_route(a, got)
+    assert all(torch.equal(got[n], again[n]) for n in got)
