@@ -62,9 +62,9 @@ int pick_ranges(int cols, int tiles, int per_sm) {
 // experts, 128 ranges, bf16 13.7 and 51; at four ranges both take as long), but
 // costs the host 2 us, and a call from Python takes the host about 16 us
 // without it.  So a pass that the GPU is through with in that time does without
-// (the first two shapes after the large one: 18.3 and 16.2 us a call, 18.3 and
-// 16.3), as long as one CTA has no more than 20 ranges to add.  How long the
-// GPU takes goes by x's bytes, and, with many experts, by the products
+// (1001 x 1032 above: 18.3 us a call with the launch, 16.2 without; 2048 x 1024:
+// 18.3 and 16.3), as long as one CTA has no more than 20 ranges to add.  How
+// long the GPU takes goes by x's bytes and, with many experts, by the products
 // (us a call with the launch and without):
 //   bytes: fp32, 8 experts, 2048 x 2048 (16 MB) 18.1 and 16.2, 4096 x 1536 (24
 //   MB) 18.5 and 20.1; bf16, 16 experts, 6000 x 1024 (12 MB) 18.8 and 18.1, 8192

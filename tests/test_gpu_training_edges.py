@@ -459,3 +459,84 @@ def test_route_backward_around_the_summing_launch(T, d, E, dtype):
     got, again = M.moe_route_backward(**a), M.moe_route_backward(**a)
     _check_route(a, got)
     assert all(torch.equal(got[n], again[n]) for n in got)
+
+
+# --------------------------------------------------- rows narrower than a tile
+@pytest.mark.parametrize("E", [8, 30, 64])
+@pytest.mark.parametrize("d", [8, 24, 56, 72])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_route_backward_of_narrow_rows_past_the_small_batches(d, E, dtype):
+    from test_gpu_training import _check_route, _route_case
+    a = _route_case(1100, d, E, 2, dtype, "softmax_topk", 1.0, True, True, "some", True)
+    whole = [torch.full((1100 * d + 128,), 7, dtype=a["x"].dtype, device=DEV),
+             torch.full((d * E + 128,), 7.0, device=DEV)]
+    got = M.moe_route_backward(**a, dx=whole[0][64:-64].view(1100, d),
+                               dWg=whole[1][64:-64].view(d, E))
+    _check_route(a, got)
+    assert all((w[:64] == 7).all() and (w[-64:] == 7).all() for w in whole)
+
+
+# ----------------------------------------------- elements past 2^31, bytes 2^32
+def _philox(first, count, seed, offset):
+    """The 16-bit lanes of counters first .. first + count - 1 (Salmon et al.)."""
+    u32, u64 = np.uint32, np.uint64
+    n = np.arange(first, first + count, dtype=u64)
+    ctr = [n.astype(u32), (n >> u64(32)).astype(u32), np.full(n.shape, offset, u32),
+           np.zeros(n.shape, u32)]
+    key = [seed, 0]
+    for _ in range(10):
+        lo, hi = ctr[0].astype(u64) * u64(0xD2511F53), ctr[2].astype(u64) * u64(0xCD9E8D57)
+        ctr = [(hi >> u64(32)).astype(u32) ^ ctr[1] ^ u32(key[0]), hi.astype(u32),
+               (lo >> u64(32)).astype(u32) ^ ctr[3] ^ u32(key[1]), lo.astype(u32)]
+        key = [(key[0] + 0x9E3779B9) % 2 ** 32, (key[1] + 0xBB67AE85) % 2 ** 32]
+    return np.ascontiguousarray(np.stack(ctr, 1)).view(np.uint16)
+
+
+def test_offsets_past_32_bits():
+    """The last rows of tensors of more than 2^31 elements, against calls on
+    copies of those rows."""
+    T, d, E, k, n = 560000, 4096, 8, 2, 700  # 2.3 G elements, 4.6 GB
+    g = _gen(8)
+    big = torch.empty((T, d), dtype=torch.bfloat16, device=DEV)
+    for t in range(0, T, 40000):
+        big[t:t + 40000] = _randn(g, min(40000, T - t), d, dtype=torch.bfloat16)
+    tail = slice(T - n, T)
+    # combine: every slot's row is one of the last n of o
+    pos = (T - n + torch.randperm(n, generator=g, device=DEV)).int().view(n // k, k)
+    gate = torch.rand((n // k, k), generator=g, device=DEV)
+    rng = torch.tensor([3, 4], device=DEV)
+    part = big[tail].clone()
+    near = (pos - (T - n)).contiguous()
+    y = M.moe_combine_dropout(big, pos, gate, 0.1, rng)
+    assert torch.equal(y, M.moe_combine_dropout(part, near, gate, 0.1, rng))
+    dy = _randn(g, n // k, d, dtype=torch.bfloat16)
+    d_o = torch.zeros_like(big)
+    d_o, dgate = M.moe_combine_dropout_backward(dy, big, pos, gate, 0.1, rng, d_o=d_o)
+    want_o, want_g = M.moe_combine_dropout_backward(dy, part, near, gate, 0.1, rng)
+    assert torch.equal(d_o[tail], want_o) and torch.equal(dgate, want_g)
+    assert not d_o[:n].any()
+    # as many tokens: the generator's counter and y's rows
+    pos = torch.full((T, 1), -1, device=DEV).int()
+    pos[tail] = torch.arange(n, device=DEV).int()[:, None]
+    one = torch.ones((T, 1), device=DEV)
+    y = M.moe_combine_dropout(part, pos, one, 0.25, rng, y=d_o)
+    # element c of token t: counter (t d + c) / 8, here past 2^28
+    words = _philox((T - n) * d // 8, n * d // 8, 3, 4)
+    kept = torch.from_numpy(words.reshape(n, d) >= oracle.dropout_threshold(0.25)).to(DEV)
+    scaled = (part.float() * (65536 / (65536 - oracle.dropout_threshold(0.25)))).bfloat16()
+    assert torch.equal(y[tail], torch.where(kept, scaled, 0))
+    del y
+    # router: the last tokens' dx, and dW_g of a gradient at those tokens alone
+    idx = torch.randint(0, E, (T, 1), generator=g, device=DEV).int()
+    dgate = torch.zeros((T, 1), device=DEV)
+    dgate[tail] = _randn(g, n, 1)
+    zero = torch.zeros((E, T), device=DEV)
+    Wg = _randn(g, d, E, dtype=torch.bfloat16)
+    got = M.moe_route_backward(big, Wg, idx, one, dgate, zero, gating="softmax_topk", dx=d_o)
+    a = dict(idx=idx[tail].contiguous(), gate=one[tail].contiguous(),
+             dgate=dgate[tail].contiguous(), scores=zero[:, tail].contiguous(),
+             gating="softmax_topk")
+    want = M.moe_route_backward(part, Wg, **a)
+    assert torch.equal(got["dx"][tail], want["dx"]) and not got["dx"][:n].any()
+    size = np64(part.abs()).T @ (np.eye(E)[a["idx"][:, 0].cpu().numpy()] * np.abs(np64(a["dgate"])))
+    assert np.all(np.abs(np64(got["dWg"]) - np64(want["dWg"])) <= 2 * (n + 8) * U32 * size)
