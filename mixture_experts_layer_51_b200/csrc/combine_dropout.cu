@@ -15,11 +15,17 @@
 // one (token, slot), so the scatter of d_o writes each row once.
 //
 // Bound by HBM: the kept rows of o, y or dy, the residual, d_o, each once.
-// Measured on one B200 (floors at 6.56 TB/s in brackets), p = 0.1, bf16:
-// forward with residual 8192 x 4096 top-2 42.4 us (40.9), top-4 60.6 (61.4),
-// 16384 x 2048 top-8 98.5 us (102.4); backward 8192 x 4096 top-2 54.2 us (51.2;
-// 53.2 without dropout, so the generator hides behind the copies), top-4 95.9
-// (92.1), 16384 x 2048 top-8 180 us (174).  What made the difference: all loads of a sweep before any
+// Measured on one B200 in a graph (floors at 6.56 TB/s in brackets), p = 0.1,
+// bf16: forward with residual 8192 x 4096 top-2 42.4 us (40.9), top-4 61.5
+// (61.4), 16384 x 2048 top-8 100.7 us (102.4); backward 8192 x 4096 top-2 54.6 us
+// (51.1; 53.5 without dropout, so the generator hides behind the copies), top-4
+// 97.4 (92.1), 16384 x 2048 top-8 180 us (174).  fp32, 8192 x 4096: forward with
+// residual top-2 78.9 us (81.8), top-4 117 (123), top-8 195 (205); backward top-2
+// 103 (102), top-4 187 (184), top-8 370 (348).
+// The backward pass writes the rows of d_o that a kept slot owns, and its time
+// is that of these rows: a reader that takes whole 128-row blocks has to clear
+// the others itself (at most 127 rows an expert).
+// What made the difference: all loads of a sweep before any
 // arithmetic (156 -> 106 us on the top-8 forward), plain instead of
 // evict-first loads (192 -> 185 us on the top-8 backward), and four sweeps a
 // warp (57.5 -> 55.8 us on 8192 x 4096).  More resident warps through fewer
@@ -350,8 +356,8 @@ int pick_warp_bits(int T, int d, int ch) {
 }
 
 // Rows of at most 16 chunks take eight lanes of a warp, so that its other
-// lanes work on other rows (100000 x 64, top-2: forward 39.7 -> 10.0 us,
-// backward 48.0 -> 12.3; with a row width known only at run time the wide rows
+// lanes work on other rows (100000 x 64, top-2, bf16: forward 39.7 -> 10.1 us
+// without a residual, 10.6 with one, backward 48.0 -> 12.6; with a row width known only at run time the wide rows
 // lose: 98 -> 115 us on 16384 x 2048 top-8).
 bool narrow(int d) { return d <= 128; }
 

@@ -21,7 +21,7 @@
 // floating-point atomics).
 //
 // dz is a launch of its own because every column block needs it: 5.6 MB of
-// scores and gates in, 128 to 384 bytes a token out (bf16 terms), 7 us for
+// scores and gates in, 128 to 384 bytes a token out (bf16 terms), 7 to 8 us for
 // 16384 tokens of 64 experts beside the products' first loads, of which about
 // 3 are its arithmetic.  Blocks of 32 tokens with eight threads a token beat
 // 64 with four (48.3 -> 46.7 us for the whole pass), and 64 registers a thread
@@ -57,9 +57,9 @@ int pick_ranges(int cols, int tiles, int per_sm) {
 // The ranges of dW_g are added by the last CTA of a column block, or by a
 // launch over all SMs.  The launch is quicker on the GPU from about five
 // ranges on (in a graph, with and without it: 16384 x 2048, 64 experts, 9
-// ranges, bf16 40.0 and 42.1 us; 1001 x 1032, 8 experts, 8 ranges, bf16 8.3 and
+// ranges, bf16 40.2 and 42.7 us; 1001 x 1032, 8 experts, 8 ranges, bf16 8.3 and
 // 9.8; 2048 x 1024, 8 experts, 16 ranges, fp32 9.5 and 11.6; 16384 x 64, 64
-// experts, 128 ranges, bf16 13.7 and 51; at four ranges both take as long), but
+// experts, 128 ranges, bf16 14.2 and 52; at four ranges both take as long), but
 // costs the host 2 us, and a call from Python takes the host about 16 us
 // without it.  So a pass that the GPU is through with in that time does without
 // (1001 x 1032 above: 18.3 us a call with the launch, 16.2 without; 2048 x 1024:

@@ -22,10 +22,12 @@
 // MMAs have landed, its block of dx (and its columns of dW_g) filled with NaN.
 //
 // Measured on one B200, all launches of the backward pass (floors at
-// 6.56 TB/s in brackets): 8192 x 4096, 8 experts, with dx_acc 39.8 us (30.8),
-// without 29.6 (20.6); 16384 x 2048 without dx_acc: 32 experts 36.6 us, 64
-// experts 39.6 (21.3), 40.0 with a mask that leaves out one token in six.  A
-// tile takes 1.45 us there, what its 64 KB take at the HBM rate of 144 CTAs;
+// 6.56 TB/s in brackets): 8192 x 4096, 8 experts, with dx_acc 40.0 us (30.8),
+// without 29.5 (20.6); 16384 x 2048 without dx_acc: 32 experts 37.1 us, 64
+// experts 40.2 (21.3), 41.5 with a mask that leaves out one token in six.  A
+// tile takes 1.5 us there, of which its 64 KB take 1.45 at the HBM rate of 144
+// CTAs (with dz in two terms in dx's product instead of three, the masked pass
+// took 39.9; dx then was off by 2^-17 of its terms where they cancel);
 // the rest is the dz kernel (7 us, which the first tiles' x is loaded behind)
 // and about 7 us of start, last tile and sums.  On fp32 FMA the same passes
 // took 181 and 778 us.  A second epilogue group and stores from a warp of

@@ -674,12 +674,14 @@ class MoELayer:
         stream of the layer's device: (y, loss, step) with y = residual +
         dropout_p(layer(x)), the balance loss [1] weighted by coef (mask: see
         moe_balance_loss), and ``step``, the dict of intermediates that
-        backward_combine and backward_router read (xp, h, o, offsets and kept_counts among them,
-        for a backward pass of the experts; dev_error is the experts' error
-        word, as moe_grouped_ffn returned it).  x, mask and rng are held, not
-        copied: none may change before the backward pass.  Nothing is recorded
+        backward_combine and backward_router read (xp, h, o, offsets and
+        kept_counts among them, for a backward pass of the experts; dev_error
+        is the experts' error word, as moe_grouped_ffn returned it).  x, mask
+        and rng are held, not copied: none may change before the backward pass.  Nothing is recorded
         for autograd: tensors that require a gradient are refused outside
-        torch.no_grad()."""
+        torch.no_grad().  The mask concerns the router's loss and gradients:
+        padding tokens are routed, computed and combined like the others, so
+        the caller's dy of them should be zero."""
         _tensor(x, "x", self.dtype, (x.shape[0], self.d), self.device.index)
         for name in ("Wg", "bias", "W1", "W3", "W2"):
             _refuse_autograd(getattr(self, name), name)
@@ -714,7 +716,10 @@ class MoELayer:
         """The router's gradients after backward_combine, as a dict: through
         the gates and the balance loss (dloss [1]: its gradient, None for 1).
         dxp: the gradient of the permuted tokens step["xp"] from the experts'
-        own backward pass; dx then holds both.  step["router_error"] is the
+        own backward pass; dx then holds both (the tokens' sums of dxp are
+        rounded to the layer dtype, as a gradient of x from the experts alone
+        would be, and once more with the router's part added).
+        step["router_error"] is the
         kernels' error word (int32 [1] on the device, 0 unless one gave up on a
         bounded wait; dx and dWg hold NaN then)."""
         dx_acc = None
